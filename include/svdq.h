@@ -210,7 +210,9 @@ SVDQ_API int svdq_export_weights(const svdq_weights* w, uint8_t* codes, void* sc
                                  void* L2, float* inv_lambda, float* lambda);
 
 /* Sticky device error word of the current device: bit 0 = a bounded wait ran
- * out in the activation kernel, bit 1 = in a GEMM kernel.  Reading clears it.
+ * out in the activation kernel, bit 1 = in a GEMM kernel, bit 4 = in the
+ * attention kernel; bit 3 = a cache operator met an index or a length out of
+ * range and left that element out (each call says what).  Reading clears it.
  * Returns the word (>= 0) or -SVDQ_ERR_CUDA.  Synchronizes the device. */
 SVDQ_API int svdq_get_error(void);
 
@@ -272,6 +274,151 @@ SVDQ_API const char* svdq_status_string(int status);
  *   FLOP = SMs * steps * 4 * 2 * 128 * 256 * (64 for NVFP4, 32 for INT4).
  * Asynchronous; returns SVDQ_ERR_INVALID_ARG for a bad format or steps < 1. */
 SVDQ_API int svdq_tensor_peak(int fmt, long long steps, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over keys and values held in 4 bits.
+ *
+ * What runs between the QKV projection and the output projection of a block:
+ * the projection's rows are normed and rotated (svdq_qk_norm_rope), keys and
+ * values go into a paged cache in one of the layer's 4-bit formats
+ * (svdq_kv_append), and the queries attend over it (svdq_kv_attention).
+ * svdq_kv_plan derives the row offsets, positions, slots and block-table
+ * entries of a batch from its request lengths.  All calls are asynchronous on
+ * `stream`, never allocate and never synchronize (the first call on a device
+ * sets kernel attributes: make it before any stream capture).  bf16 rows are
+ * 16-byte aligned with strides (in elements) that are multiples of 8; heads of
+ * a row are contiguous.  Indices in device memory (slots, pages, positions,
+ * lengths) are checked by the kernels: an element with one out of range is left
+ * out, as each call says, and bit 3 of svdq_get_error is set.
+ *
+ * A cache is caller-owned memory of num_pages * svdq_kv_page_bytes bytes,
+ * [num_pages][kv_heads] blocks of
+ *     key codes    page_size x head_dim / 2 bytes, element 2i in the low nibble
+ *     key scales   page_size x head_dim / g: E4M3 bytes (g = 16 for NVFP4, 32 for
+ *                  FP4 g32) or fp16 (g = 64, INT4)
+ *     value codes, value scales: the same
+ * Slot s is token s % page_size of page s / page_size.  Formats: SVDQ_NVFP4,
+ * SVDQ_FP4G32, SVDQ_INT4, with the quantizer of svdq_quantize_act (groups along
+ * head_dim, no smoothing).  head_dim 64 or 128; page_size a power of two from 16
+ * to 256; 1 <= kv_heads <= 1024; num_pages < 2^31. */
+typedef struct {
+  int fmt, kv_heads, head_dim, page_size;
+  long long num_pages;
+  void* pool;              /* device, 16-byte aligned */
+} svdq_kv_cache;
+
+/* Bytes of one page (all heads, keys and values).  `pool` is not looked at. */
+SVDQ_API int svdq_kv_page_bytes(const svdq_kv_cache* cache, size_t* bytes);
+
+/* Batch plan.  Request b has kv_lens[b] tokens in the cache and brings q_lens[b]
+ * new ones.  Writes cu_q (batch + 1 row offsets), total_lens (kv + q), the new
+ * entries of block_table (batch rows of table_width pages, table_stride apart):
+ * ceil((kv + q) / page) - ceil(kv / page) pages per request from free_pages in
+ * request order, and per row the position and the slot.  Rows behind the last
+ * request (a padded batch) get position -1 and slot -1, which the other calls
+ * skip.  *used = free pages taken.  Entries of block_table that hold cached
+ * tokens are read, all others but the new ones are left alone; total_lens and
+ * cu_q must not overlap the inputs.  The same inputs give the same results, so a
+ * repeated call writes the same entries again.
+ * Out of range (bit 3): a negative length or a total past 2^31 - 1 counts as no
+ * new tokens; tokens past `rows` are dropped (cu_q and total_lens say so); a page
+ * past table_width or past free_count is not entered (or entered as -1), its
+ * tokens get slot -1.  batch <= 16384. */
+typedef struct {
+  const int* q_lens;       /* batch */
+  const int* kv_lens;      /* batch */
+  int* block_table;
+  long long table_stride;
+  int table_width;
+  const int* free_pages;
+  int free_count;
+  int batch, rows, page_size;
+  int* cu_q;               /* batch + 1 */
+  int* total_lens;         /* batch */
+  int* positions;          /* rows */
+  int64_t* slots;          /* rows */
+  int* used;               /* 1 */
+} svdq_kv_plan_desc;
+SVDQ_API int svdq_kv_plan(const svdq_kv_plan_desc* desc, void* stream);
+
+/* RMS norm of each query and key head, y = x / sqrt(mean x^2 + eps) * weight
+ * (skipped if norm == 0), and the rotation of its leading rot_dim elements by
+ * the angles of the row's position: (a, b) -> (a cos - b sin, b cos + a sin) for
+ * the pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.  `table` holds
+ * table_rows rows of rot_dim / 2 cosines and rot_dim / 2 sines (fp32); row m
+ * uses row positions[m], or row m if positions is NULL.  fp32 inside, one
+ * rounding to bf16.  The outputs may be the inputs (same pointer and stride) but
+ * must not overlap them otherwise.  A row with a position below 0 is left as it
+ * is, as is (bit 3) one with a position >= table_rows.  head_dim a multiple of 16
+ * from 16 to 256, rot_dim a multiple of 16 from 0 to head_dim; q_heads or
+ * k_heads may be 0. */
+typedef struct {
+  const void* q;           /* bf16 rows x q_heads x head_dim, q_stride elements between rows */
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  const void* q_weight;    /* bf16 head_dim, or NULL: ones */
+  const void* k_weight;
+  const float* table;      /* table_rows x rot_dim; may be NULL if rot_dim == 0 */
+  const int* positions;    /* rows, or NULL */
+  int table_rows;
+  int rows, q_heads, k_heads, head_dim, rot_dim;
+  int norm, interleaved;
+  float eps;
+} svdq_qk_norm_rope_desc;
+SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* desc, void* stream);
+
+/* Quantize the keys and values of M rows (bf16 M x kv_heads x head_dim, strides
+ * in elements) into their slots.  A row with a slot below 0 is skipped, as is
+ * (bit 3) one past the pool.  The slots >= 0 of a call must differ; what two
+ * rows leave in the same slot is unspecified.  The values must be finite. */
+SVDQ_API int svdq_kv_append(const svdq_kv_cache* cache, const void* k, const void* v, long long k_stride,
+                            long long v_stride, const int64_t* slots, int M, void* stream);
+
+/* The values that the codes of M slots stand for, code * scale, contiguous
+ * M x kv_heads x head_dim, fp32 (out_fp32 != 0, exact) or bf16 (exact but for
+ * INT4, which is rounded).  A row with a slot below 0, or (bit 3) past the pool,
+ * reads as zeros. */
+SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int M, int out_fp32, void* k, void* v,
+                          void* stream);
+
+/* Attention of the new tokens' queries over the cache:
+ *     out = softmax(scale q k^T) v,    lse = log sum exp(scale q k^T)
+ * Request b has rows cu_q[b] .. cu_q[b + 1] - 1, its keys are the tokens
+ * 0 .. kv_lens[b] - 1 of the cache (the new ones included) at
+ * block_table[b][t / page_size].  Query i of n sits at position
+ * kv_lens[b] - n + i; with `causal` it sees keys up to its own position, with
+ * window > 0 only those past position - window.  A query that sees no key gives
+ * out = 0 and lse = -inf.  q_heads is a multiple of kv_heads; query head h reads
+ * key head h / (q_heads / kv_heads).  Products, softmax and sums are fp32; the
+ * weights exp(s - max) are rounded to fp16 for the product with the values.
+ * Rows outside cu_q[0] .. cu_q[batch] - 1 are left as they are.  What the cache holds past
+ * kv_lens[b] is never used, whatever its bytes.  Out of range (bit 3): cu_q is
+ * clamped to 0 .. rows, kv_lens to what the table row holds, and the keys of a page
+ * outside the pool are masked.  `workspace` (svdq_kv_attention_workspace_bytes,
+ * 256-byte aligned, no initial contents) is scratch of this call: calls that may
+ * overlap on the GPU need one each. */
+typedef struct {
+  svdq_kv_cache cache;
+  const void* q;           /* bf16 rows x q_heads x head_dim */
+  long long q_stride;
+  void* out;               /* bf16 rows x q_heads x head_dim */
+  long long out_stride;
+  float* lse;              /* rows x q_heads, or NULL */
+  const int* cu_q;         /* batch + 1 */
+  const int* kv_lens;      /* batch */
+  const int* block_table;
+  long long table_stride;
+  int table_width;
+  int batch, rows, q_heads;
+  int causal, window;
+  float scale;
+  void* workspace;
+} svdq_kv_attention_desc;
+/* Depends on cache (pool aside), q_heads, rows and batch only. */
+SVDQ_API int svdq_kv_attention_workspace_bytes(const svdq_kv_attention_desc* desc, size_t* bytes);
+SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* desc, void* stream);
 
 SVDQ_API void svdq_weights_destroy(svdq_weights* w);
 

@@ -1,0 +1,262 @@
+// kv_api.cuh -- host side of the cache operators of include/svdq.h (batch plan,
+// query/key norm and rotation, append, read, attention): argument checks and
+// launches.  Included by svdq_api.cu, whose error macros, device table and
+// launch helper it uses.
+#pragma once
+
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
+#include "kv_plan.cuh"
+#include "qk_norm_rope.cuh"
+
+namespace {
+
+inline int log2_exact(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+// Kernel attributes of the cache operators, once per device.
+std::atomic<bool> g_kv_set[kMaxDevices];
+
+int kv_device(int* dev) {
+  const int rc = current_device(dev);
+  if (rc) return rc;
+  if (g_kv_set[*dev].load(std::memory_order_acquire)) return SVDQ_OK;
+  std::lock_guard<std::mutex> lk(g_mutex);
+  if (g_kv_set[*dev].load(std::memory_order_relaxed)) return SVDQ_OK;
+  SVDQ_CUDA(cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (2 * kPlanMaxRequests + 1) * static_cast<int>(sizeof(int))));
+  g_kv_set[*dev].store(true, std::memory_order_release);
+  return SVDQ_OK;
+}
+
+// SVDQ_OK and the geometry of a cache description, or why it is refused.
+int kv_geometry(const svdq_kv_cache* c, KvGeom* g, bool need_pool) {
+  if (c == nullptr || (c->fmt != SVDQ_NVFP4 && c->fmt != SVDQ_INT4 && c->fmt != SVDQ_FP4G32)) return SVDQ_ERR_INVALID_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || c->kv_heads < 1 || c->kv_heads > 1024 || c->page_size < 16 ||
+      c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0)
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (c->num_pages < 0 || c->num_pages > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (need_pool && (c->pool == nullptr || !aligned16(c->pool))) return SVDQ_ERR_INVALID_ARG;
+  const int codes = c->page_size * c->head_dim / 2, scales = c->page_size * kv_scale_bytes(c->fmt, c->head_dim);
+  g->pool = static_cast<uint8_t*>(c->pool);
+  g->num_pages = c->num_pages;
+  g->heads = c->kv_heads;
+  g->D = c->head_dim;
+  g->page = c->page_size;
+  g->page_log2 = log2_exact(c->page_size);
+  g->ks = codes;
+  g->vc = codes + scales;
+  g->vs = 2 * codes + scales;
+  g->head_bytes = 2 * (codes + scales);
+  return SVDQ_OK;
+}
+
+// rows of heads x D bf16 values whose loads are whole 16-byte words
+bool rows_ok(const void* p, long long stride) { return p != nullptr && aligned16(p) && stride % 8 == 0 && stride >= 0; }
+
+}  // namespace
+
+extern "C" {
+
+SVDQ_API int svdq_kv_page_bytes(const svdq_kv_cache* cache, size_t* bytes) {
+  KvGeom g;
+  const int rc = kv_geometry(cache, &g, false);
+  if (rc) return rc;
+  if (bytes == nullptr) return SVDQ_ERR_INVALID_ARG;
+  *bytes = static_cast<size_t>(g.head_bytes) * g.heads;
+  return SVDQ_OK;
+}
+
+SVDQ_API int svdq_kv_plan(const svdq_kv_plan_desc* d, void* stream) {
+  if (d == nullptr || d->batch < 0 || d->rows < 0 || d->table_width < 0 || d->free_count < 0 || d->table_stride < d->table_width)
+    return SVDQ_ERR_INVALID_ARG;
+  if (d->batch > kPlanMaxRequests || d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)) != 0)
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (d->cu_q == nullptr || d->used == nullptr || (d->batch > 0 && (d->q_lens == nullptr || d->kv_lens == nullptr || d->total_lens == nullptr)) ||
+      (d->batch > 0 && d->table_width > 0 && d->block_table == nullptr) || (d->free_count > 0 && d->free_pages == nullptr) ||
+      (d->rows > 0 && (d->positions == nullptr || d->slots == nullptr)))
+    return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  const int rc = kv_device(&dev);
+  if (rc) return rc;
+  PlanParams p;
+  p.q_lens = d->q_lens;
+  p.kv_lens = d->kv_lens;
+  p.table = d->block_table;
+  p.table_stride = d->table_stride;
+  p.width = d->table_width;
+  p.free_pages = d->free_pages;
+  p.free_count = d->free_count;
+  p.batch = d->batch;
+  p.rows = d->rows;
+  p.page_log2 = log2_exact(d->page_size);
+  p.cu_q = d->cu_q;
+  p.total = d->total_lens;
+  p.positions = d->positions;
+  p.slots = reinterpret_cast<long long*>(d->slots);
+  p.used = d->used;
+  const int ctas = std::max(1, (d->rows + kPlanRows - 1) / kPlanRows);
+  const size_t smem = (2 * static_cast<size_t>(d->batch) + 1) * sizeof(int);
+  SVDQ_CUDA(launch_pdl(kv_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream), 0u, p));
+  return SVDQ_OK;
+}
+
+SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* d, void* stream) {
+  if (d == nullptr || d->rows < 0 || d->q_heads < 0 || d->k_heads < 0) return SVDQ_ERR_INVALID_ARG;
+  if (d->head_dim < 16 || d->head_dim > 256 || d->head_dim % 16 != 0 || d->rot_dim < 0 || d->rot_dim > d->head_dim ||
+      d->rot_dim % 16 != 0 || d->q_heads > 65536 || d->k_heads > 65536)
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (d->rows == 0 || d->q_heads + d->k_heads == 0) return SVDQ_OK;
+  const long long qn = static_cast<long long>(d->q_heads) * d->head_dim, kn = static_cast<long long>(d->k_heads) * d->head_dim;
+  if (d->q_heads > 0 && (!rows_ok(d->q, d->q_stride) || !rows_ok(d->q_out, d->q_out_stride) || (d->rows > 1 && d->q_out_stride < qn)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (d->k_heads > 0 && (!rows_ok(d->k, d->k_stride) || !rows_ok(d->k_out, d->k_out_stride) || (d->rows > 1 && d->k_out_stride < kn)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (d->rot_dim > 0 && (d->table == nullptr || d->table_rows < 0)) return SVDQ_ERR_INVALID_ARG;
+  if (d->rot_dim > 0 && d->positions == nullptr && d->table_rows < d->rows) return SVDQ_ERR_INVALID_ARG;
+  if ((d->q_weight != nullptr && !aligned16(d->q_weight)) || (d->k_weight != nullptr && !aligned16(d->k_weight))) return SVDQ_ERR_INVALID_ARG;
+  if (d->norm && !(d->eps >= 0.f)) return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  const int rc = kv_device(&dev);
+  if (rc) return rc;
+  NormRopeParams p;
+  p.q = static_cast<const __nv_bfloat16*>(d->q);
+  p.k = static_cast<const __nv_bfloat16*>(d->k);
+  p.q_out = static_cast<__nv_bfloat16*>(d->q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(d->k_out);
+  p.q_stride = d->q_stride;
+  p.k_stride = d->k_stride;
+  p.q_out_stride = d->q_out_stride;
+  p.k_out_stride = d->k_out_stride;
+  p.q_weight = static_cast<const __nv_bfloat16*>(d->q_weight);
+  p.k_weight = static_cast<const __nv_bfloat16*>(d->k_weight);
+  p.table = d->table;
+  p.positions = d->positions;
+  p.table_rows = d->table_rows;
+  p.rows = d->rows;
+  p.q_heads = d->q_heads;
+  p.k_heads = d->k_heads;
+  p.D = d->head_dim;
+  p.rot = d->rot_dim;
+  p.norm = d->norm != 0;
+  p.interleaved = d->interleaved != 0;
+  p.eps = d->eps;
+  p.lanes_log2 = log2_exact((d->head_dim + 7) / 8);
+  const int heads = d->q_heads + d->k_heads;
+  p.chunk = 1;
+  p.chunks = heads;
+  const long long threads = (static_cast<long long>(d->rows) * p.chunks) << p.lanes_log2;
+  const long long ctas = (threads + kNormThreads - 1) / kNormThreads;
+  if (ctas > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  SVDQ_CUDA(launch_pdl(qk_norm_rope_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), 0,
+                       static_cast<cudaStream_t>(stream), 0u, p));
+  return SVDQ_OK;
+}
+
+SVDQ_API int svdq_kv_append(const svdq_kv_cache* cache, const void* k, const void* v, long long k_stride,
+                            long long v_stride, const int64_t* slots, int M, void* stream) {
+  KvGeom g;
+  int rc = kv_geometry(cache, &g, M > 0);
+  if (rc) return rc;
+  if (M < 0) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;
+  if (slots == nullptr || !rows_ok(k, k_stride) || !rows_ok(v, v_stride)) return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  if ((rc = kv_device(&dev))) return rc;
+  const long long threads = static_cast<long long>(M) * 2 * g.heads * (g.D / 16);
+  const long long ctas = (threads + kAppendThreads - 1) / kAppendThreads;
+  if (ctas > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid(static_cast<unsigned>(ctas)), blk(kAppendThreads);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(k);
+  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(v);
+  const long long* sl = reinterpret_cast<const long long*>(slots);
+  auto* kernel = cache->fmt == SVDQ_NVFP4 ? kv_append_kernel<0> : cache->fmt == SVDQ_INT4 ? kv_append_kernel<1> : kv_append_kernel<2>;
+  SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, g, kp, vp, k_stride, v_stride, sl, M));
+  return SVDQ_OK;
+}
+
+SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int M, int out_fp32, void* k, void* v,
+                          void* stream) {
+  KvGeom g;
+  int rc = kv_geometry(cache, &g, M > 0);
+  if (rc) return rc;
+  if (M < 0) return SVDQ_ERR_INVALID_ARG;
+  if (M == 0) return SVDQ_OK;
+  if (slots == nullptr || k == nullptr || v == nullptr || !aligned16(k) || !aligned16(v)) return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  if ((rc = kv_device(&dev))) return rc;
+  const long long threads = static_cast<long long>(M) * 2 * g.heads * (g.D / 16);
+  const long long ctas = (threads + kAppendThreads - 1) / kAppendThreads;
+  if (ctas > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid(static_cast<unsigned>(ctas)), blk(kAppendThreads);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long* sl = reinterpret_cast<const long long*>(slots);
+  if (out_fp32) {
+    auto* kernel = cache->fmt == SVDQ_NVFP4 ? kv_read_kernel<0, float> : cache->fmt == SVDQ_INT4 ? kv_read_kernel<1, float> : kv_read_kernel<2, float>;
+    SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, g, sl, M, static_cast<float*>(k), static_cast<float*>(v)));
+  } else {
+    auto* kernel = cache->fmt == SVDQ_NVFP4 ? kv_read_kernel<0, __nv_bfloat16>
+                   : cache->fmt == SVDQ_INT4 ? kv_read_kernel<1, __nv_bfloat16> : kv_read_kernel<2, __nv_bfloat16>;
+    SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, g, sl, M, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v)));
+  }
+  return SVDQ_OK;
+}
+
+SVDQ_API int svdq_kv_attention_workspace_bytes(const svdq_kv_attention_desc* d, size_t* bytes) {
+  if (d == nullptr || bytes == nullptr || d->rows < 0 || d->batch < 0) return SVDQ_ERR_INVALID_ARG;
+  KvGeom g;
+  const int rc = kv_geometry(&d->cache, &g, false);
+  if (rc) return rc;
+  *bytes = 0;
+  return SVDQ_OK;
+}
+
+SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
+  if (d == nullptr) return SVDQ_ERR_INVALID_ARG;
+  AttnParams p;
+  int rc = kv_geometry(&d->cache, &p.g, d->rows > 0);
+  if (rc) return rc;
+  if (d->rows < 0 || d->batch < 0 || d->window < 0 || d->table_width < 0 || d->table_stride < d->table_width) return SVDQ_ERR_INVALID_ARG;
+  if (d->q_heads < 1 || d->q_heads % p.g.heads != 0 || d->q_heads > 65536) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (!(d->scale == d->scale) || std::isinf(d->scale)) return SVDQ_ERR_INVALID_ARG;
+  if (d->rows == 0 || d->batch == 0) return SVDQ_OK;
+  if (!rows_ok(d->q, d->q_stride) || !rows_ok(d->out, d->out_stride) || d->cu_q == nullptr || d->kv_lens == nullptr ||
+      (d->table_width > 0 && d->block_table == nullptr) ||
+      (d->rows > 1 && d->out_stride < static_cast<long long>(d->q_heads) * p.g.D))
+    return SVDQ_ERR_INVALID_ARG;
+  int dev;
+  if ((rc = kv_device(&dev))) return rc;
+  p.q = static_cast<const __nv_bfloat16*>(d->q);
+  p.q_stride = d->q_stride;
+  p.out = static_cast<__nv_bfloat16*>(d->out);
+  p.out_stride = d->out_stride;
+  p.lse = d->lse;
+  p.cu_q = d->cu_q;
+  p.kv_lens = d->kv_lens;
+  p.table = d->block_table;
+  p.table_stride = d->table_stride;
+  p.width = d->table_width;
+  p.batch = d->batch;
+  p.rows = d->rows;
+  p.q_heads = d->q_heads;
+  p.causal = d->causal != 0;
+  p.window = d->window;
+  p.scale = d->scale;
+  const long long units = static_cast<long long>(d->rows) * d->q_heads;
+  if ((units + 3) / 4 > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid(static_cast<unsigned>((units + 3) / 4)), blk(128);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void (*kernel)(AttnParams);
+  if (p.g.D == 64)
+    kernel = d->cache.fmt == SVDQ_NVFP4 ? kv_attn_rows_kernel<0, 64> : d->cache.fmt == SVDQ_INT4 ? kv_attn_rows_kernel<1, 64> : kv_attn_rows_kernel<2, 64>;
+  else
+    kernel = d->cache.fmt == SVDQ_NVFP4 ? kv_attn_rows_kernel<0, 128> : d->cache.fmt == SVDQ_INT4 ? kv_attn_rows_kernel<1, 128> : kv_attn_rows_kernel<2, 128>;
+  SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, p));
+  return SVDQ_OK;
+}
+
+}  // extern "C"

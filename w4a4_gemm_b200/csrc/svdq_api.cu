@@ -1448,3 +1448,5 @@ SVDQ_API int svdq_export_weights(const svdq_weights* w, uint8_t* codes, void* sc
 SVDQ_API void svdq_weights_destroy(svdq_weights* w) { free_weights(w); }
 
 }  // extern "C"
+
+#include "kv_api.cuh"
