@@ -398,7 +398,7 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
  * clamped to 0 .. rows, kv_lens to what the table row holds, and the keys of a page
  * outside the pool are masked.  `workspace` (svdq_kv_attention_workspace_bytes,
  * 256-byte aligned, no initial contents) is scratch of this call: calls that may
- * overlap on the GPU need one each. */
+ * overlap on the GPU need one each.  batch <= 65536. */
 typedef struct {
   svdq_kv_cache cache;
   const void* q;           /* bf16 rows x q_heads x head_dim */

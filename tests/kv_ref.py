@@ -10,7 +10,10 @@ Tolerances, per element (half a bf16 step is 2^-8 of the value, half an fp16 ste
                     products, the rotation's two products and one addition, the
                     table's own rounding: under 16 = 2^4 fp32 steps in all.
   attention         2^-8 |o| for the output, and relative to A = sum p |v| / sum p:
-                    2^-11 for the fp16 weights, 2 ds for the scores, 2^-20 for
+                    2^-11 for the fp16 weights, 2^-40 sum |v| / sum p for the
+                    smallest of them (the largest weight is held as 2^15, the
+                    smallest fp16 step is 2^-24, so half of it is 2^-40 of the
+                    largest weight), 2 ds for the scores, 2^-20 for
                     exp2 and the division, n 2^-23 for n keys' fp32 sums (a tensor
                     core may truncate: a whole step each), where ds, the error of
                     a score, is (D + 8) 2^-23 max_t scale |q|.|k_t|.
@@ -94,6 +97,7 @@ def attention(q, keys, values, scale, causal, window):
         A = w @ np.abs(v) / total[:, None]
         ds = (D + 8) * 2.0 ** -23 * big
         tol_o[:, h] += 2.0 ** -8 * np.abs(out[:, h]) + (2.0 ** -11 + 2 * ds + 2.0 ** -20 + kv * 2.0 ** -23)[:, None] * A
+        tol_o[:, h] += 2.0 ** -40 * (seen @ np.abs(v)) / total[:, None]
         tol_l[:, h] += ds + 2.0 ** -20 * (1 + np.abs(np.where(any_, lse[:, h], 0))) + kv * 2.0 ** -23
     return out, lse, tol_o, tol_l
 

@@ -90,9 +90,9 @@ def test_refused_attentions(S):
     call = lambda **kw: S.lib().svdq_kv_attention(ctypes.byref(S._KvAttentionDesc(*[{**good, **kw}[n] for n in names])), None)  # noqa: E731
     for bad in (dict(q=None), dict(q=0x1008), dict(q_stride=252), dict(out=None), dict(out_stride=248), dict(cu_q=None), dict(kv_lens=None),
                 dict(block_table=None), dict(table_stride=3), dict(batch=-1), dict(rows=-1), dict(window=-1), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(cache=cache(S, pool=None)), dict(cache=cache(S, fmt=3)), dict(table_width=-1)):
+                dict(scale=float("inf")), dict(cache=cache(S, pool=None)), dict(workspace=None), dict(workspace=0x1080), dict(cache=cache(S, fmt=3)), dict(table_width=-1)):
         assert call(**bad) == 1, bad
-    for bad in (dict(q_heads=3), dict(q_heads=0), dict(cache=cache(S, dim=32)), dict(cache=cache(S, page=20))):
+    for bad in (dict(q_heads=3), dict(q_heads=0), dict(batch=65537), dict(cache=cache(S, dim=32)), dict(cache=cache(S, page=20))):
         assert call(**bad) == 2, bad
     assert call(rows=0) == 0 and call(batch=0) == 0
     assert S.lib().svdq_kv_attention(None, None) == 1

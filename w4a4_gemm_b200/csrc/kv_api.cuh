@@ -17,6 +17,40 @@ inline int log2_exact(int v) {
   return l;
 }
 
+// ------------------------------------------------------------- attention ---
+constexpr int kMaxAttnCtas = 148 * 4;      // the most CTAs of a launch: words and slots of the workspace
+constexpr int kAttnMaxBatch = 65536;       // the sums of 32 requests each are scanned in shared memory (16 KB)
+constexpr size_t kAttnCounterBytes = (kMaxAttnCtas * sizeof(unsigned long long) + 255) & ~static_cast<size_t>(255);
+
+// Blocks of 8 query rows that a decode tile has: two where a key head has more than 8 rows per request on average.
+int dec_blocks(const svdq_kv_attention_desc* d) {
+  const long long rep = d->q_heads / d->cache.kv_heads;
+  return d->batch > 0 && static_cast<long long>(d->rows) * rep > 8LL * d->batch ? 2 : 1;
+}
+int dec_ctas_per_sm(int nb) { return nb == 1 ? 4 : 3; }
+
+using AttnKernel = void (*)(AttnParams);
+
+template <int FMT>
+AttnKernel dec_kernel_of(int D, int nb) {
+  if (D == 64) return nb == 1 ? kv_attn_decode_kernel<FMT, 64, 1> : kv_attn_decode_kernel<FMT, 64, 2>;
+  return nb == 1 ? kv_attn_decode_kernel<FMT, 128, 1> : kv_attn_decode_kernel<FMT, 128, 2>;
+}
+AttnKernel dec_kernel(int fmt, int D, int nb) {
+  return fmt == SVDQ_NVFP4 ? dec_kernel_of<kFmtNvfp4>(D, nb) : fmt == SVDQ_INT4 ? dec_kernel_of<kFmtInt4>(D, nb) : dec_kernel_of<kFmtFp4g32>(D, nb);
+}
+
+// 48 bits that differ from launch to launch (a counter spread by an odd multiplier and
+// the shifts of splitmix64's finalizer), above 16 zero bits.
+unsigned long long launch_nonce() {
+  static std::atomic<unsigned long long> count{0};
+  unsigned long long z = (count.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull;
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  z ^= z >> 31;
+  return (z | 0x10000ull) & ~0xFFFFull;
+}
+
 // Kernel attributes of the cache operators, once per device.
 std::atomic<bool> g_kv_set[kMaxDevices];
 
@@ -28,6 +62,12 @@ int kv_device(int* dev) {
   if (g_kv_set[*dev].load(std::memory_order_relaxed)) return SVDQ_OK;
   SVDQ_CUDA(cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (2 * kPlanMaxRequests + 1) * static_cast<int>(sizeof(int))));
+  if (g_dev[*dev].sms * 4 > kMaxAttnCtas) return SVDQ_ERR_CUDA;   // the workspace is laid out for 148 SMs
+  for (int fmt : {SVDQ_NVFP4, SVDQ_INT4, SVDQ_FP4G32})
+    for (int D : {64, 128})
+      for (int nb : {1, 2})
+        SVDQ_CUDA(cudaFuncSetAttribute(dec_kernel(fmt, D, nb), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(dec_smem_bytes(fmt, D, nb))));
   g_kv_set[*dev].store(true, std::memory_order_release);
   return SVDQ_OK;
 }
@@ -211,7 +251,8 @@ SVDQ_API int svdq_kv_attention_workspace_bytes(const svdq_kv_attention_desc* d, 
   KvGeom g;
   const int rc = kv_geometry(&d->cache, &g, false);
   if (rc) return rc;
-  *bytes = 0;
+  if (d->q_heads < 1 || d->q_heads % g.heads != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  *bytes = kAttnCounterBytes + static_cast<size_t>(kMaxAttnCtas) * 2 * 8 * dec_blocks(d) * (g.D + 2) * sizeof(float);
   return SVDQ_OK;
 }
 
@@ -228,6 +269,8 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
       (d->table_width > 0 && d->block_table == nullptr) ||
       (d->rows > 1 && d->out_stride < static_cast<long long>(d->q_heads) * p.g.D))
     return SVDQ_ERR_INVALID_ARG;
+  if (d->batch > kAttnMaxBatch) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (d->workspace == nullptr || (reinterpret_cast<uintptr_t>(d->workspace) & 255u)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
   p.q = static_cast<const __nv_bfloat16*>(d->q);
@@ -243,19 +286,23 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
   p.batch = d->batch;
   p.rows = d->rows;
   p.q_heads = d->q_heads;
+  p.rep = d->q_heads / p.g.heads;
   p.causal = d->causal != 0;
   p.window = d->window;
   p.scale = d->scale;
-  const long long units = static_cast<long long>(d->rows) * d->q_heads;
-  if ((units + 3) / 4 > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid(static_cast<unsigned>((units + 3) / 4)), blk(128);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  void (*kernel)(AttnParams);
-  if (p.g.D == 64)
-    kernel = d->cache.fmt == SVDQ_NVFP4 ? kv_attn_rows_kernel<0, 64> : d->cache.fmt == SVDQ_INT4 ? kv_attn_rows_kernel<1, 64> : kv_attn_rows_kernel<2, 64>;
-  else
-    kernel = d->cache.fmt == SVDQ_NVFP4 ? kv_attn_rows_kernel<0, 128> : d->cache.fmt == SVDQ_INT4 ? kv_attn_rows_kernel<1, 128> : kv_attn_rows_kernel<2, 128>;
-  SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, p));
+  p.budget = wait_budget();
+  p.nonce = launch_nonce();
+  p.counters = static_cast<unsigned long long*>(d->workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + kAttnCounterBytes);
+  p.min_units = 1;
+  const int nb = dec_blocks(d);
+  // enough CTAs for the most units that these rows and this table can hold
+  const long long tiles = std::min<long long>((static_cast<long long>(d->rows) * p.rep + 8 * nb - 1) / (8 * nb) + d->batch,
+                                              static_cast<long long>(d->rows) * p.rep);
+  const long long units = tiles * p.g.heads * std::max<long long>(1, ((static_cast<long long>(p.width) << p.g.page_log2) + kDecUnit - 1) / kDecUnit + 1);
+  const int ctas = static_cast<int>(std::min<long long>(units, static_cast<long long>(g_dev[dev].sms) * dec_ctas_per_sm(nb)));
+  SVDQ_CUDA(launch_pdl(dec_kernel(d->cache.fmt, p.g.D, nb), dim3(ctas), dim3(kDecThreads), dec_smem_bytes(d->cache.fmt, p.g.D, nb),
+                       static_cast<cudaStream_t>(stream), 0u, p));
   return SVDQ_OK;
 }
 

@@ -6,6 +6,27 @@
 // over the keys t that query i sees: t < kv_len, with `causal` t <= pos_i, with a
 // window t > pos_i - window, where pos_i = kv_len - q_len + i.  A query that sees
 // no key gives o = 0 and lse = -inf.
+//
+// This kernel is for few query rows per key head (decode): it reads the cache once
+// at the rate of HBM.  A warp takes 32 keys at a time, all D, from a ring of bulk
+// copies of its own, turns the codes into operand fragments in registers, and
+// keeps a running maximum and sum per row; the warps of a CTA take turns along the
+// keys and join at the end of an item.  The products run transposed,
+//   S^T = K q^T,   O^T += V^T P^T,
+// so that the keys (16 at a time) fill the 16-row side of mma.sync.m16n8k16 and
+// the few query rows its 8-column side.
+//   * FP4 formats: code * scale is exact in fp16 (2 + 4 significant bits), both for
+//     keys and values.
+//   * INT4: the codes are exact in fp16 and bf16.  A key group's scale multiplies
+//     its partial scores in fp32; a value group's scale multiplies the weights,
+//     which then span the range of fp16 scales times [0, 1], so they enter the
+//     product as a bf16 pair hi + lo (16 bits).
+//   * Queries are bf16 and scores are products with fp16 keys: a row is divided by
+//     the power of two of its largest element, which leaves an exact fp16 value for
+//     every element down to 2^-17 of the largest and an error below 2^-36 of it
+//     for the rest.  The factor goes into the scores' scale.
+//   * Weights are exp2(x - max + 15), at most 2^15, so fp16 holds them to 2^-11
+//     relative down to 2^-29 of the largest and to 2^-40 absolute.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -14,104 +35,666 @@
 #include <cstdint>
 
 #include "kv_cache.cuh"
+#include "kv_sched.cuh"
 #include "svdq_ptx.cuh"
 
 namespace svdq {
 
-struct AttnParams {
-  KvGeom g;
-  const __nv_bfloat16* q;
-  long long q_stride;            // elements between rows
-  __nv_bfloat16* out;
-  long long out_stride;
-  float* lse;                    // [rows][q_heads], or null
-  const int* cu_q;               // [batch + 1]
-  const int* kv_lens;            // [batch]
-  const int* table;
-  long long table_stride;
-  int width;
-  int batch, rows, q_heads;
-  int causal, window;
-  float scale;
-};
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecChunk = 32;                       // keys of a warp's step
+constexpr int kDecUnit = kDecChunk * kDecWarps;     // keys of a unit of work
+constexpr int kDecStages = 3;
 
-// One warp per (row, query head), D / 32 neighbouring elements per lane, one key at a time.
+__host__ __device__ constexpr int dec_stage_bytes(int fmt, int D) {
+  return 2 * kDecChunk * (D / 2 + kv_scale_bytes(fmt, D));
+}
+__host__ __device__ constexpr uint32_t dec_smem_bytes(int fmt, int D, int NB) {
+  return static_cast<uint32_t>(kDecWarps * kDecStages * dec_stage_bytes(fmt, D) + kDecWarps * kDecStages * 8 /* barriers */ +
+                               kDecWarps * kDecStages * 4 /* pieces */ + 2 * kDecWarps * 8 * NB * 4 /* max, sum */ + 128);
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight E2M1 codes -> four fp16 pairs, code 2i in the low half of pair i.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t* h) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Eight 4-bit two's complement codes -> four fp16 pairs (code i, code i + 4): u = code ^ 8
+// under the exponent of 1024 is 1024 + u (or 1024 + 16 u), minus 1032 (or / 16, minus 72).
+__device__ __forceinline__ void int4x8_to_f16(uint32_t w, uint32_t* h) {
+  const uint32_t x = w ^ 0x88888888u, y = x >> 8;
+  const uint32_t p[4] = {(x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x64006400u, (y & 0x000F000Fu) | 0x64006400u,
+                         (y & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(p[i]), "r"(0x64086408u));                               // 1032
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[i + 1]) : "r"(p[i + 1]), "r"(0x2C002C00u), "r"(0xD480D480u));  // 1/16, -72
+  }
+}
+
+// Key of row m (0..15) of a 16-key block: pairs (2t, 2t + 1) are keys t and 4 + (t ^ 1), so that the rows
+// of a fragment load lie in both halves of the 32 banks.
+__device__ __forceinline__ int key_of_row(int m) {
+  const int t = (m & 7) >> 1;
+  return (m & 8) + ((m & 1) ? 4 + (t ^ 1) : t);
+}
+
+// Queries of one 8-row block as B fragments of K q^T.  Lane (r, t) holds elements of row r; pair k of
+// register kk matches the key fragments below.  `f` receives 2^e of the row.
 template <int FMT, int D>
-__global__ void __launch_bounds__(128) kv_attn_rows_kernel(const AttnParams p) {
-  griddep_launch_dependents();
-  griddep_wait();
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int row = static_cast<int>(unit / p.q_heads), h = static_cast<int>(unit % p.q_heads);
-  if (row >= p.rows) return;
-  int lo = 0, hi = p.batch;
-  if (row < p.cu_q[0] || row >= p.cu_q[p.batch]) return;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_q[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int b = lo;
-  const int n = p.cu_q[b + 1] - p.cu_q[b];
-  long long kv = p.kv_lens[b];
-  if (kv < 0 || kv > static_cast<long long>(p.width) * p.g.page) {
-    if (lane == 0) raise_error(kErrIndex);
-    kv = kv < 0 ? 0 : static_cast<long long>(p.width) * p.g.page;
-  }
-  const long long pos = kv - n + (row - p.cu_q[b]);
-  const long long end = p.causal ? (pos + 1 < kv ? pos + 1 : kv) : kv;
-  long long begin = p.window > 0 ? pos - p.window + 1 : 0;
-  if (begin < 0) begin = 0;
-  const int kvh = h / (p.q_heads / p.g.heads);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+__device__ __forceinline__ void load_queries(const __nv_bfloat16* row, bool live, int t, uint32_t (&qf)[D / 8], float& f) {
+  constexpr int N = D / 4;                            // elements of this lane
+  float v[N];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[row * p.q_stride + h * D + lane * E + e]) * p.scale;
-    o[e] = 0.f;
-  }
-  for (long long t = begin; t < end; ++t) {
-    const int page = p.table[b * p.table_stride + (t >> p.g.page_log2)];
-    if (page < 0 || page >= p.g.num_pages) {
-      if (lane == 0) raise_error(kErrIndex);
-      continue;
-    }
-    const int off = static_cast<int>(t & (p.g.page - 1));
-    const uint8_t* blk = p.g.pool + kv_block(p.g, page, kvh);
-    float kvv[2][E];
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  if (live) {
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const uint8_t* at = blk + (side ? p.g.vc : 0);
-      const uint8_t* sc = at + p.g.ks + off * kv_scale_bytes(FMT, D);
-      const int grp = lane * E / kv_group(FMT);
-      float s;
-      if (FMT == kFmtInt4)
-        s = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(sc + 2 * grp)));
-      else
-        s = e4m3_value(sc[grp]);
+    for (int i = 0; i < N; i += 8) {
+      // FP4 at D = 128: 32 neighbouring elements per lane; else 16 of each group of 64
+      const int d = (FMT != kFmtInt4 && D == 128) ? 32 * t + i : 64 * (i / 16) + 16 * t + i % 16;
+      const uint4 w = *reinterpret_cast<const uint4*>(row + d);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t byte = at[off * (D / 2) + (lane * E + e) / 2];
-        const uint32_t nib = (e & 1) ? byte >> 4 : byte & 15u;
-        kvv[side][e] = s * (FMT == kFmtInt4 ? static_cast<float>(static_cast<int>(nib << 28) >> 28) : e2m1_value(nib));
+      for (int j = 0; j < 4; ++j) {
+        v[i + 2 * j] = bf16_lo(u[j]);
+        v[i + 2 * j + 1] = bf16_hi(u[j]);
       }
     }
-    float d = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) d = fmaf(q[e], kvv[0][e], d);
-#pragma unroll
-    for (int x = 16; x > 0; x /= 2) d += __shfl_xor_sync(0xffffffffu, d, x);
-    const float m2 = fmaxf(m, d);
-    const float c = expf(m - m2), w = expf(d - m2);
-    l = l * c + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, kvv[1][e], o[e] * c);
-    m = m2;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  float amax = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out[row * p.out_stride + h * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
-  if (p.lse != nullptr && lane == 0) p.lse[static_cast<long long>(row) * p.q_heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // 2^e with 2^12 <= amax / 2^e < 2^13; both factors stay normal
+  const int e = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 127 - 12, -120), 120);
+  f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // FP4 pairs are neighbours (2j, 2j + 1); INT4 pairs are (j, j + 4)
+      const float a = FMT == kFmtInt4 ? v[i + j] : v[i + 2 * j];
+      const float b = FMT == kFmtInt4 ? v[i + j + 4] : v[i + 2 * j + 1];
+      qf[i / 2 + j] = pack_f16x2(a * inv, b * inv);
+    }
+  }
+}
+
+// Scores of 16 keys (rows `key`, `key + 8` of this lane) against NB blocks of 8 rows, before the rows' factors.
+template <int FMT, int D, int NB>
+__device__ __forceinline__ void key_scores(const uint8_t* codes, const uint8_t* scales, int key, int t, const uint32_t (&qf)[NB][D / 8],
+                                           float (&s)[NB][4]) {
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
+  if constexpr (FMT == kFmtInt4) {
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) {
+      const uint2 lo = *reinterpret_cast<const uint2*>(codes + key * (D / 2) + 32 * g + 8 * t);
+      const uint2 hi = *reinterpret_cast<const uint2*>(codes + (key + 8) * (D / 2) + 32 * g + 8 * t);
+      float part[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[nb][i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t x[4], y[4];
+        int4x8_to_f16(w ? lo.y : lo.x, x);
+        int4x8_to_f16(w ? hi.y : hi.x, y);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(part[nb], a, qf[nb][8 * g + 4 * w + 2 * h], qf[nb][8 * g + 4 * w + 2 * h + 1]);
+        }
+      }
+      const float s0 = __half2float(*reinterpret_cast<const __half*>(scales + key * (D / 32) + 2 * g));
+      const float s1 = __half2float(*reinterpret_cast<const __half*>(scales + (key + 8) * (D / 32) + 2 * g));
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        s[nb][0] = fmaf(part[nb][0], s0, s[nb][0]);
+        s[nb][1] = fmaf(part[nb][1], s0, s[nb][1]);
+        s[nb][2] = fmaf(part[nb][2], s1, s[nb][2]);
+        s[nb][3] = fmaf(part[nb][3], s1, s[nb][3]);
+      }
+    }
+  } else {
+    constexpr int W = D / 32;                         // words (8 codes) of this lane per key
+    uint32_t lo[W], hi[W];
+    const uint8_t* at = codes + key * (D / 2) + 4 * W * t;
+    if constexpr (W == 4) {
+      const uint4 a = *reinterpret_cast<const uint4*>(at), b = *reinterpret_cast<const uint4*>(at + 8 * (D / 2));
+      lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w;
+      hi[0] = b.x, hi[1] = b.y, hi[2] = b.z, hi[3] = b.w;
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(at), b = *reinterpret_cast<const uint2*>(at + 8 * (D / 2));
+      lo[0] = a.x, lo[1] = a.y;
+      hi[0] = b.x, hi[1] = b.y;
+    }
+    // scale pairs (s, s): of word w's group, for the keys `key` (lo) and `key + 8` (hi)
+    constexpr int SB = kv_scale_bytes(FMT, D);
+    constexpr int PER = FMT == kFmtNvfp4 ? 2 : 4;     // words of a group
+    constexpr int GL = W / PER > 0 ? W / PER : 1;     // groups that this lane touches
+    uint32_t sl[GL], sh[GL];
+    if constexpr (GL == 2) {
+      const uint32_t a = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(scales + key * SB + 2 * t));
+      const uint32_t b = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(scales + (key + 8) * SB + 2 * t));
+      sl[0] = __byte_perm(a, a, 0x1010), sl[1] = __byte_perm(a, a, 0x3232);
+      sh[0] = __byte_perm(b, b, 0x1010), sh[1] = __byte_perm(b, b, 0x3232);
+    } else {
+      const int g = t * W / PER;
+      sl[0] = e4m3x2_to_f16(scales[key * SB + g] * 0x101u);
+      sh[0] = e4m3x2_to_f16(scales[(key + 8) * SB + g] * 0x101u);
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      uint32_t x[4], y[4];
+      e2m1x8_to_f16(lo[w], x);
+      e2m1x8_to_f16(hi[w], y);
+      const uint32_t s0 = sl[GL == 2 ? w / 2 : 0], s1 = sh[GL == 2 ? w / 2 : 0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = hmul2_u(x[i], s0);
+        y[i] = hmul2_u(y[i], s1);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_f16_16816(s[nb], a, qf[nb][4 * w + 2 * h], qf[nb][4 * w + 2 * h + 1]);
+      }
+    }
+  }
+}
+
+// O^T += V^T P^T for 16 keys.  w[nb][0..3]: the weights of this lane's score elements (keys of rows r and
+// r + 8, columns 2t and 2t + 1).  `usable`: keys below it are real, scales of the others count as zero.
+template <int FMT, int D, int NB>
+__device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* scales, int r, int t, int usable,
+                                           const float (&w)[NB][4], float (&o)[NB][D / 16][4]) {
+  int key[4];                                         // keys of contraction indices 2t, 2t + 1, 2t + 8, 2t + 9
+  key[0] = t, key[1] = 4 + (t ^ 1), key[2] = 8 + t, key[3] = 12 + (t ^ 1);
+  if constexpr (FMT == kFmtInt4) {
+    // words 8 r' .. of each group of 64: m-tile j of a group has row r = element 8 r + 2j, row r + 8 the next
+    const int k0 = key_of_row(r), k1 = k0 + 8;
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) {
+      const float s0 = k0 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k0 * (D / 32) + 2 * g)) : 0.f;
+      const float s1 = k1 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k1 * (D / 32) + 2 * g)) : 0.f;
+      uint32_t bh[NB][2], bl[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float s = half ? s1 : s0;
+          const float a = w[nb][2 * half] * s, b = w[nb][2 * half + 1] * s;
+          const uint32_t hi = pack_bf16x2(a, b);
+          const uint32_t lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
+          bh[nb][half] = movmatrix(hi);
+          bl[nb][half] = movmatrix(lo);
+        }
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint32_t*>(codes + key[i] * (D / 2) + 32 * g + 4 * r) ^ 0x88888888u;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {          // codes 0..3, 4..7 of the words
+        const uint32_t x = __byte_perm(c[0], c[1], half ? 0x7632 : 0x5410);
+        const uint32_t y = __byte_perm(c[2], c[3], half ? 0x7632 : 0x5410);
+        uint32_t ux[4], uy[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                 // 128 + u in bf16, minus 136
+          const uint32_t px = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u, py = ((y >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+          asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(ux[i]) : "r"(px), "r"(0x43084308u));
+          asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(uy[i]) : "r"(py), "r"(0x43084308u));
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t a[4] = {ux[2 * j], ux[2 * j + 1], uy[2 * j], uy[2 * j + 1]};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_bf16_16816(o[nb][4 * g + 2 * half + j], a, bh[nb][0], bh[nb][1]);
+            mma_bf16_16816(o[nb][4 * g + 2 * half + j], a, bl[nb][0], bl[nb][1]);
+          }
+        }
+      }
+    }
+  } else {
+    uint32_t b[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      b[nb][0] = movmatrix(pack_f16x2(w[nb][0], w[nb][1]));
+      b[nb][1] = movmatrix(pack_f16x2(w[nb][2], w[nb][3]));
+    }
+    // row r holds D / 8 neighbouring elements from D / 8 * r; m-tile j: row r = element 2j of them, row r + 8 the next
+    constexpr int W = D / 64;                         // words per key
+    constexpr int SB = kv_scale_bytes(FMT, D);
+    const int g = r * (D / 8) / kv_group(FMT);
+    uint32_t c[4][W], sc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* at = codes + key[i] * (D / 2) + (D / 16) * r;
+      if constexpr (W == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        c[i][0] = v.x, c[i][1] = v.y;
+      } else {
+        c[i][0] = *reinterpret_cast<const uint32_t*>(at);
+      }
+      sc[i] = key[i] < usable ? scales[key[i] * SB + g] : 0u;
+    }
+    const uint32_t s01 = e4m3x2_to_f16(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16(sc[2] | (sc[3] << 8));
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      // bytes (key a's code, key b's code) of the even and the odd elements
+      const uint32_t m = 0x0F0F0F0Fu;
+      const uint32_t e01 = (c[0][v] & m) | ((c[1][v] << 4) & ~m), o01 = ((c[0][v] >> 4) & m) | (c[1][v] & ~m);
+      const uint32_t e23 = (c[2][v] & m) | ((c[3][v] << 4) & ~m), o23 = ((c[2][v] >> 4) & m) | (c[3][v] & ~m);
+      uint32_t f[4][4];
+      e2m1x8_to_f16(e01, f[0]);
+      e2m1x8_to_f16(o01, f[1]);
+      e2m1x8_to_f16(e23, f[2]);
+      e2m1x8_to_f16(o23, f[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a[4] = {hmul2_u(f[0][j], s01), hmul2_u(f[1][j], s01), hmul2_u(f[2][j], s23), hmul2_u(f[3][j], s23)};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[nb][4 * v + j], a, b[nb][0], b[nb][1]);
+      }
+    }
+  }
+}
+
+// First of the two neighbouring elements of row r (and row r + 8) of accumulator tile j.
+template <int FMT, int D>
+__device__ __forceinline__ int value_element(int r, int j) {
+  if (FMT == kFmtInt4) return 64 * (j / 4) + 8 * r + 2 * (j % 4);
+  return (D / 8) * r + 2 * j;
+}
+
+template <int FMT, int D, int NB>
+__global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_kernel(const AttnParams p) {
+  constexpr int RT = 8 * NB;
+  constexpr int STAGE = dec_stage_bytes(FMT, D);
+  constexpr int SB = kv_scale_bytes(FMT, D);
+  constexpr int PITCH = D + 4;                        // floats of a row of the joined sums
+  static_assert(RT * PITCH * 4 <= kDecStages * STAGE, "a warp's sums fit its ring");
+  extern __shared__ __align__(128) uint8_t dec_smem[];
+  const int warp = static_cast<int>(warp_id()), lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+  uint8_t* ring = dec_smem + warp * kDecStages * STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(dec_smem + kDecWarps * kDecStages * STAGE) + warp * kDecStages;
+  int* pieces = reinterpret_cast<int*>(dec_smem + kDecWarps * kDecStages * (STAGE + 8)) + warp * kDecStages;
+  float* row_max = reinterpret_cast<float*>(dec_smem + kDecWarps * kDecStages * (STAGE + 12));   // [warps][RT]
+  float* row_sum = row_max + kDecWarps * RT;
+  __shared__ Share share;
+  __shared__ int last_flag;
+
+  griddep_launch_dependents();
+  if (lane == 0) {
+    for (int s = 0; s < kDecStages; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
+  }
+  griddep_wait();
+  find_share<RT, kDecUnit>(p, reinterpret_cast<long long*>(dec_smem), &share);
+  fence_proxy_async_smem();                           // the scan's words lie under the rings
+  int count = share.count;
+  if (count == 0) return;
+  int b = share.b, h = share.h, rt = share.rt, unit = share.unit;
+  const long long total = share.total, begin = share.begin;
+  const int ctas = share.ctas;
+  long long at = begin;                               // unit number of the current segment's first unit
+  Request req = load_request(p, b);
+  int it = 0;                                         // chunks that this warp has used so far
+  bool dead = false;                                  // a wait ran out
+
+  while (true) {
+    int k0, k1;
+    tile_keys<RT, kDecUnit>(p, req, rt, k0, k1);
+    const int units = max(1, (k1 - k0 + kDecUnit - 1) / kDecUnit);
+    const int here = min(units - unit, count);
+    const int first = k0 + unit * kDecUnit;           // keys of this segment
+    const int limit = min(k1, here >= units - unit ? k1 : first + here * kDecUnit);
+
+    // this lane's score columns: rows 2t, 2t + 1 of each block
+    const long long rows = static_cast<long long>(req.n) * p.rep;
+    uint32_t qf[NB][D / 8];
+    float factor[NB][2];
+    int lo_key[NB][2], hi_key[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const long long row = static_cast<long long>(rt) * RT + nb * 8 + r;
+      const bool live = row < rows;
+      const int i = live ? static_cast<int>(row / p.rep) : 0, hq = live ? h * p.rep + static_cast<int>(row % p.rep) : 0;
+      float f;
+      load_queries<FMT, D>(p.q + (req.row0 + i) * p.q_stride + hq * D, live, t, qf[nb], f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        factor[nb][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4) * (p.scale * 1.4426950408889634f);
+        const long long rj = static_cast<long long>(rt) * RT + nb * 8 + 2 * t + j;
+        const int ij = static_cast<int>(min(rj, rows - 1) / p.rep);
+        const int pos = req.kv - req.n + ij;
+        hi_key[nb][j] = p.causal ? min(req.kv, pos + 1) : req.kv;
+        lo_key[nb][j] = p.window > 0 ? pos - p.window + 1 : 0;
+      }
+    }
+    // keys that every row of the tile sees
+    const int i_first = static_cast<int>(static_cast<long long>(rt) * RT / p.rep);
+    const int i_last = static_cast<int>((min((rt + 1LL) * RT, rows) - 1) / p.rep);
+    const int all_hi = p.causal ? min(req.kv, req.kv - req.n + i_first + 1) : req.kv;
+    const int all_lo = p.window > 0 ? req.kv - req.n + i_last - p.window + 1 : 0;
+
+    float m[NB][2], l[NB][2], o[NB][D / 16][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[nb][j] = -INFINITY;
+        l[nb][j] = 0.f;
+      }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nb][d][i] = 0.f;
+    }
+
+    const int* table = p.table + b * p.table_stride;
+    const int mine = first + warp * kDecChunk;        // this warp's first chunk; the next is kDecUnit on
+    const int chunks = limit > mine ? (limit - mine + kDecUnit - 1) / kDecUnit : 0;
+
+    // Copies of the chunk `c` into stage (it + c) % kDecStages: lane 0 (and lane 1 with pages of 16) each
+    // bring the part that lies in one page; a part at or past `limit` or in a bad page is left out.
+    const int piece = p.g.page >= kDecChunk ? kDecChunk : 16;
+    const bool copier = lane * piece < kDecChunk;
+    auto page_of = [&](int c) {
+      const long long key = static_cast<long long>(mine) + static_cast<long long>(c) * kDecUnit + lane * piece;
+      if (!copier || c >= chunks || key >= limit) return -1;
+      const int page = table[key >> p.g.page_log2];
+      if (page < 0 || page >= p.g.num_pages) {
+        raise_error(kErrIndex);
+        return -1;
+      }
+      return page;
+    };
+    auto issue = [&](int c, int page) {
+      const int st = (it + c) % kDecStages;
+      const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
+      constexpr int kPieceBytes16 = 2 * 16 * (D / 2 + SB);
+      if (lane == 0) {
+        pieces[st] = piece == kDecChunk ? ((good & 1) ? 3 : 0) : static_cast<int>(good & 3);
+        mbar_arrive_expect_tx(&bars[st], __popc(good) * (piece / 16) * kPieceBytes16);
+      }
+      __syncwarp();
+      if (page >= 0) {
+        const int key = mine + c * kDecUnit + lane * piece;
+        const int off = key & (p.g.page - 1);
+        const uint8_t* blk = p.g.pool + kv_block(p.g, page, h);
+        uint8_t* dst = ring + st * STAGE;
+        const int k = lane * piece;
+        bulk_load(dst + k * (D / 2), blk + off * (D / 2), piece * (D / 2), &bars[st]);
+        bulk_load(dst + kDecChunk * (D / 2) + k * SB, blk + p.g.ks + off * SB, piece * SB, &bars[st]);
+        bulk_load(dst + STAGE / 2 + k * (D / 2), blk + p.g.vc + off * (D / 2), piece * (D / 2), &bars[st]);
+        bulk_load(dst + STAGE / 2 + kDecChunk * (D / 2) + k * SB, blk + p.g.vs + off * SB, piece * SB, &bars[st]);
+      }
+    };
+    if (!dead) {
+      for (int c = 0; c < min(chunks, kDecStages - 1); ++c) issue(c, page_of(c));
+      int page = page_of(kDecStages - 1);
+      int issued = min(chunks, kDecStages - 1);
+      for (int c = 0; c < chunks; ++c) {
+        __syncwarp();                                 // every lane has left the stage that is filled next
+        if (c + kDecStages - 1 < chunks) {
+          issue(c + kDecStages - 1, page);
+          ++issued;
+        }
+        page = page_of(c + kDecStages);               // looked up a step ahead of its copy
+        const int st = (it + c) % kDecStages;
+        if (!warp_wait(&bars[st], ((it + c) / kDecStages) & 1, p.budget, nullptr)) {
+          if (lane == 0) raise_error(kErrWaitAttn);
+          dead = true;
+          for (; c < issued; ++c)                     // copies in flight land before the ring is given up
+            warp_wait(&bars[(it + c) % kDecStages], ((it + c) / kDecStages) & 1, drain_budget(p.budget), nullptr);
+          break;
+        }
+        const uint8_t* kc = ring + st * STAGE;
+        const uint8_t* vc = kc + STAGE / 2;
+        const uint8_t* ks = kc + kDecChunk * (D / 2);
+        const uint8_t* vs = vc + kDecChunk * (D / 2);
+        const int base = mine + c * kDecUnit;
+        const int have = pieces[st];
+        float s[2][NB][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) key_scores<FMT, D, NB>(kc + u * 16 * (D / 2), ks + u * 16 * SB, key_of_row(r), t, qf, s[u]);
+        const bool whole = have == 3 && base >= all_lo && base + kDecChunk <= all_hi && base + kDecChunk <= limit;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][nb][i] *= factor[nb][i & 1];
+        if (!whole) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = base + 16 * u + key_of_row(r) + (i & 2 ? 8 : 0);
+                const bool see = ((have >> u) & 1) && key < limit && key < hi_key[nb][i & 1] && key >= lo_key[nb][i & 1];
+                if (!see) s[u][nb][i] = -INFINITY;
+              }
+        }
+        // maximum of each column over the chunk, then weights
+        float w[2][NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float top[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            top[j] = fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], x));
+          }
+          if (__any_sync(0xffffffffu, top[0] > m[nb][0] || top[1] > m[nb][1])) {
+            float c2[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float m2 = fmaxf(m[nb][j], top[j]);
+              c2[j] = m2 == -INFINITY ? 1.f : ex2(m[nb][j] - m2);
+              m[nb][j] = m2;
+              l[nb][j] *= c2[j];
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[nb][d][i] *= c2[i & 1];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float sub = m[nb][j] == -INFINITY ? 0.f : m[nb][j] - 15.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = j; i < 4; i += 2) {
+                w[u][nb][i] = ex2(s[u][nb][i] - sub);
+                l[nb][j] += w[u][nb][i];
+              }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int usable = whole ? 16 : (((have >> u) & 1) ? limit - base - 16 * u : 0);
+          add_values<FMT, D, NB>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, usable, w[u], o);
+        }
+      }
+    }
+    it += chunks;
+
+    // ------------------------------------------------ join the warps of the CTA
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], x);
+        if (r == 0) {
+          row_max[warp * RT + nb * 8 + 2 * t + j] = m[nb][j];
+          row_sum[warp * RT + nb * 8 + 2 * t + j] = l[nb][j];
+        }
+      }
+    __syncthreads();                                  // every warp has left its ring, too
+    float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = nb * 8 + 2 * t + j;
+        float top = row_max[row];
+#pragma unroll
+        for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, row_max[w * RT + row]);
+        const float c = m[nb][j] == -INFINITY ? 0.f : ex2(m[nb][j] - top);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+          *reinterpret_cast<float2*>(sums + row * PITCH + value_element<FMT, D>(r, d)) =
+              make_float2(o[nb][d][j] * c, o[nb][d][j + 2] * c);
+      }
+    __syncthreads();
+    const int live_rows = static_cast<int>(min(static_cast<long long>(RT), rows - static_cast<long long>(rt) * RT));
+    const bool split = unit > 0 || here < units;
+    const long long item = at - unit;                 // unit number of the item's first unit
+    constexpr int Q = D / 4;
+    const float* all = reinterpret_cast<const float*>(dec_smem);
+    constexpr int kWarpFloats = kDecStages * STAGE / 4;
+    float* slot = p.partials + (2ll * blockIdx.x + (at == begin ? 0 : 1)) * (RT * (D + 2));
+    for (int e = threadIdx.x; e < live_rows * Q; e += kDecThreads) {
+      const int row = e / Q, d = e % Q * 4;
+      float top = row_max[row];
+#pragma unroll
+      for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, row_max[w * RT + row]);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float mw = row_max[w * RT + row];
+        sum += mw == -INFINITY ? 0.f : row_sum[w * RT + row] * ex2(mw - top);
+        const float4 v = *reinterpret_cast<const float4*>(all + w * kWarpFloats + row * PITCH + d);
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      if (!split) {
+        const long long gr = static_cast<long long>(rt) * RT + row;
+        const int i = static_cast<int>(gr / p.rep), hq = h * p.rep + static_cast<int>(gr % p.rep);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        *reinterpret_cast<uint2*>(p.out + (req.row0 + i) * p.out_stride + hq * D + d) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (p.lse != nullptr && d == 0)
+          p.lse[static_cast<long long>(req.row0 + i) * p.q_heads + hq] =
+              sum > 0.f ? (top - 15.f + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        __stcg(reinterpret_cast<float4*>(slot + row * D + d), acc);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(slot + RT * D + 2 * row), make_float2(top, sum));
+      }
+    }
+    if (split) {
+      const int c0 = share_of(total, ctas, item), c1 = share_of(total, ctas, item + units - 1);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        last_flag = arrive_last(&p.counters[c0], p.nonce, c1 - c0 + 1);
+        __threadfence();
+      }
+      __syncthreads();
+      if (last_flag) {
+        const int slot0 = share_begin(total, ctas, c0) == item ? 2 * c0 : 2 * c0 + 1;
+        for (int e = threadIdx.x; e < live_rows * Q; e += kDecThreads) {
+          const int row = e / Q, d = e % Q * 4;
+          float top = -INFINITY;
+          for (int c = c0; c <= c1; ++c) {
+            const float* sl = p.partials + static_cast<long long>(c == c0 ? slot0 : 2 * c) * (RT * (D + 2));
+            top = fmaxf(top, __ldcg(sl + RT * D + 2 * row));
+          }
+          float sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = c0; c <= c1; ++c) {
+            const float* sl = p.partials + static_cast<long long>(c == c0 ? slot0 : 2 * c) * (RT * (D + 2));
+            const float2 ms = __ldcg(reinterpret_cast<const float2*>(sl + RT * D + 2 * row));
+            const float f = ms.x == -INFINITY ? 0.f : ex2(ms.x - top);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + row * D + d));
+            sum = fmaf(ms.y, f, sum);
+            acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+          }
+          const long long gr = static_cast<long long>(rt) * RT + row;
+          const int i = static_cast<int>(gr / p.rep), hq = h * p.rep + static_cast<int>(gr % p.rep);
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          *reinterpret_cast<uint2*>(p.out + (req.row0 + i) * p.out_stride + hq * D + d) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (p.lse != nullptr && d == 0)
+            p.lse[static_cast<long long>(req.row0 + i) * p.q_heads + hq] =
+                sum > 0.f ? (top - 15.f + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+    }
+
+    // ------------------------------------------------ the next item of the share
+    count -= here;
+    at += here;
+    if (count <= 0) break;
+    __syncthreads();                                  // the sums have been read: the rings may be filled again
+    fence_proxy_async_smem();
+    unit = 0;
+    if (++rt >= row_tiles<RT>(p, req)) {
+      rt = 0;
+      if (++h >= p.g.heads) {
+        h = 0;
+        do {
+          if (++b >= p.batch) return;                 // not reached: the share ends inside the batch
+          req = load_request(p, b);
+        } while (req.n == 0);
+      }
+    }
+  }
 }
 
 }  // namespace svdq

@@ -1,0 +1,247 @@
+// kv_sched.cuh -- how the attention kernels share their work.
+//
+// An item is one tile of RT query rows (a row is a token and one of the query
+// heads that share a key head) of one request and key head; its keys, cut into
+// units of KT, are the work.  The units of all items, in the order request, key
+// head, row tile, key, form one line that the CTAs cut into equal contiguous
+// shares, whatever the lengths: a CTA finishes whole items by itself, and an item
+// that spans CTAs is joined by the last of them to arrive.  Lengths stay on the
+// GPU: each CTA finds its share by itself, 32 requests at a time per warp.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "kv_cache.cuh"
+#include "svdq_ptx.cuh"
+
+namespace svdq {
+
+struct AttnParams {
+  KvGeom g;
+  const __nv_bfloat16* q;
+  long long q_stride;            // elements between rows
+  __nv_bfloat16* out;
+  long long out_stride;
+  float* lse;                    // [rows][q_heads], or null
+  const int* cu_q;               // [batch + 1]
+  const int* kv_lens;            // [batch]
+  const int* table;
+  long long table_stride;
+  int width;
+  int batch, rows, q_heads, rep; // rep: query heads per key head
+  int causal, window;
+  float scale;
+  float* partials;               // workspace: 2 slots per CTA of RT x D sums and RT (max, sum) pairs
+  unsigned long long* counters;  // workspace: one word per CTA
+  unsigned long long nonce;      // of this launch, in the upper 48 bits
+  int min_units;                 // units that make a CTA worth its share
+  long long budget;              // of a bounded wait, in cycles
+};
+
+struct Request {
+  int row0, n, kv;               // first row, new tokens, keys
+};
+
+// Lengths as the caller gives them, cut to what the rows and the table hold.
+__device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
+  const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], kv = p.kv_lens[b];
+  const long long cap = min(static_cast<long long>(p.width) << p.g.page_log2, 0x7fff0000LL);
+  Request r;
+  r.row0 = min(max(c0, 0), p.rows);
+  r.n = min(max(c1, r.row0), p.rows) - r.row0;
+  r.kv = static_cast<int>(min(static_cast<long long>(max(kv, 0)), cap));
+  if (c0 != r.row0 || c1 != r.row0 + r.n || kv != r.kv) raise_error(kErrIndex);
+  return r;
+}
+
+// Keys [k0, k1) that any row of tile rt sees; k0 is cut down to a multiple of KT.
+template <int RT, int KT>
+__device__ __forceinline__ void tile_keys(const AttnParams& p, const Request& r, int rt, int& k0, int& k1) {
+  const long long rows = static_cast<long long>(r.n) * p.rep;
+  const int i0 = static_cast<int>(static_cast<long long>(rt) * RT / p.rep);
+  const int i1 = static_cast<int>((min((rt + 1LL) * RT, rows) - 1) / p.rep);
+  k1 = p.causal ? max(0, min(r.kv, r.kv - r.n + i1 + 1)) : r.kv;
+  k0 = p.window > 0 ? max(0, r.kv - r.n + i0 - p.window + 1) : 0;
+  k0 = min(k0, k1) / KT * KT;
+}
+
+// Units of a tile: at least one, so that rows without keys are written too.
+template <int RT, int KT>
+__device__ __forceinline__ int tile_units(const AttnParams& p, const Request& r, int rt) {
+  int k0, k1;
+  tile_keys<RT, KT>(p, r, rt, k0, k1);
+  return max(1, (k1 - k0 + KT - 1) / KT);
+}
+
+template <int RT>
+__device__ __forceinline__ int row_tiles(const AttnParams& p, const Request& r) {
+  return static_cast<int>((static_cast<long long>(r.n) * p.rep + RT - 1) / RT);
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Units of one key head of the requests base .. base + 31, one per lane: a lane adds
+// up a few tiles by itself, and the warp goes over a long request's tiles together.
+template <int RT, int KT>
+__device__ __forceinline__ long long group_units(const AttnParams& p, int base, Request& r) {
+  const int lane = threadIdx.x & 31, b = base + lane;
+  r = Request{0, 0, 0};
+  if (b < p.batch) r = load_request(p, b);
+  const int tiles = row_tiles<RT>(p, r);
+  constexpr int kFew = 4;
+  long long mine = 0;
+  if (tiles <= kFew)
+    for (int rt = 0; rt < tiles; ++rt) mine += tile_units<RT, KT>(p, r, rt);
+  unsigned many = __ballot_sync(0xffffffffu, tiles > kFew);
+  while (many) {
+    const int src = __ffs(many) - 1;
+    many &= many - 1;
+    Request o;
+    o.row0 = 0;
+    o.n = __shfl_sync(0xffffffffu, r.n, src);
+    o.kv = __shfl_sync(0xffffffffu, r.kv, src);
+    const int n = __shfl_sync(0xffffffffu, tiles, src);
+    long long s = 0;
+    for (int rt = lane; rt < n; rt += 32) s += tile_units<RT, KT>(p, o, rt);
+    s = warp_sum(s);
+    if (lane == src) mine = s;
+  }
+  return mine;
+}
+
+__device__ __forceinline__ long long warp_inclusive(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Where a CTA's share begins, and its size.  In shared memory.
+struct Share {
+  long long total;               // units of the whole launch
+  long long begin;               // first unit of this CTA
+  int ctas;                      // CTAs that have a share
+  int count;                     // units of this CTA (0: none)
+  int b, h, rt, unit;            // the item of the first unit, and the unit inside it
+};
+
+__host__ __device__ inline long long share_begin(long long total, int ctas, int c) { return total * c / ctas; }
+
+// The CTA whose share holds unit u.
+__device__ __forceinline__ int share_of(long long total, int ctas, long long u) {
+  int c = static_cast<int>(u * ctas / total);
+  while (share_begin(total, ctas, c + 1) <= u) ++c;
+  while (share_begin(total, ctas, c) > u) --c;
+  return c;
+}
+
+// Called by all threads.  `sums` holds (batch + 31) / 32 words of shared memory.
+template <int RT, int KT>
+__device__ __forceinline__ void find_share(const AttnParams& p, long long* sums, Share* s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int groups = (p.batch + 31) / 32;
+  Request r;
+  for (int g = warp; g < groups; g += warps) {
+    const long long t = warp_sum(group_units<RT, KT>(p, 32 * g, r));
+    if (lane == 0) sums[g] = t * p.g.heads;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long total = 0;
+    for (int g = lane; g < groups; g += 32) total += sums[g];
+    total = warp_sum(total);
+    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + p.min_units - 1) / p.min_units));
+    const int c = blockIdx.x;
+    if (c >= ctas) {                          // also when there is no work at all
+      if (lane == 0) s->count = 0;
+    } else {
+      const long long begin = share_begin(total, ctas, c), end = share_begin(total, ctas, c + 1);
+      // the group of 32 requests that holds `begin`
+      long long left = begin;
+      int g = 0;
+      for (int base = 0;; base += 32) {
+        const long long v = base + lane < groups ? sums[base + lane] : 0;
+        const long long inc = warp_inclusive(v);
+        const unsigned over = __ballot_sync(0xffffffffu, inc > left);
+        if (over) {
+          const int k = __ffs(over) - 1;
+          left -= __shfl_sync(0xffffffffu, inc - v, k);
+          g = base + k;
+          break;
+        }
+        left -= __shfl_sync(0xffffffffu, inc, 31);
+        if (base + 32 >= groups) break;       // not reached: begin < total
+      }
+      // the request, the key head, the row tile
+      const long long one = group_units<RT, KT>(p, 32 * g, r);
+      const long long v = one * p.g.heads, inc = warp_inclusive(v);
+      const unsigned over = __ballot_sync(0xffffffffu, inc > left);
+      const int k = over ? __ffs(over) - 1 : 0;
+      left -= __shfl_sync(0xffffffffu, inc - v, k);
+      const long long per_head = max(1LL, __shfl_sync(0xffffffffu, one, k));
+      Request o;
+      o.row0 = 0;
+      o.n = __shfl_sync(0xffffffffu, r.n, k);
+      o.kv = __shfl_sync(0xffffffffu, r.kv, k);
+      const int h = static_cast<int>(left / per_head);
+      left -= h * per_head;
+      const int tiles = row_tiles<RT>(p, o);
+      int rt = 0;
+      for (int base = 0; base < tiles; base += 32) {
+        const long long w = base + lane < tiles ? tile_units<RT, KT>(p, o, base + lane) : 0;
+        const long long winc = warp_inclusive(w);
+        const unsigned past = __ballot_sync(0xffffffffu, winc > left);
+        if (past) {
+          const int j = __ffs(past) - 1;
+          left -= __shfl_sync(0xffffffffu, winc - w, j);
+          rt = base + j;
+          break;
+        }
+        left -= __shfl_sync(0xffffffffu, winc, 31);
+      }
+      if (lane == 0) {
+        s->total = total;
+        s->begin = begin;
+        s->ctas = ctas;
+        s->count = static_cast<int>(min(end - begin, 0x7fffffffLL));
+        s->b = 32 * g + k;
+        s->h = h;
+        s->rt = rt;
+        s->unit = static_cast<int>(left);
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- split items ---
+// An item cut between CTAs c0 .. c1 leaves a partial result per CTA: in slot 2c of
+// CTA c if the item is the first of c's share, in slot 2c + 1 otherwise (it is then
+// its last).  Counter word c0 counts arrivals.  The words need no initial value: one
+// that does not carry the launch's 48-bit nonce counts as zero, and the last CTA
+// to arrive leaves zero behind, so a graph that replays the launch starts from
+// zero too.  Sums are taken in the order of the CTAs, whoever arrives last.
+
+// One thread.  True if this is the last of `parts` arrivals.
+__device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long nonce, int parts) {
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  while (true) {
+    const unsigned long long count = (old & ~0xFFFFull) == nonce ? (old & 0xFFFFull) : 0ull;
+    const bool last = count + 1 == static_cast<unsigned long long>(parts);
+    const unsigned long long now = last ? 0ull : (nonce | (count + 1));
+    const unsigned long long seen = atomicCAS(word, old, now);
+    if (seen == old) return last;
+    old = seen;
+  }
+}
+
+}  // namespace svdq
