@@ -18,7 +18,7 @@ inline int log2_exact(int v) {
 }
 
 // ------------------------------------------------------------- attention ---
-constexpr int kMaxAttnCtas = 148 * 4;      // the most CTAs of a launch: words and slots of the workspace
+constexpr int kMaxAttnCtas = 148 * 3;      // the most CTAs of a launch: words and slots of the workspace
 constexpr int kAttnMaxBatch = 65536;       // the sums of 32 requests each are scanned in shared memory (16 KB)
 constexpr size_t kAttnCounterBytes = (kMaxAttnCtas * sizeof(unsigned long long) + 255) & ~static_cast<size_t>(255);
 
@@ -27,7 +27,7 @@ int dec_blocks(const svdq_kv_attention_desc* d) {
   const long long rep = d->q_heads / d->cache.kv_heads;
   return d->batch > 0 && static_cast<long long>(d->rows) * rep > 8LL * d->batch ? 2 : 1;
 }
-int dec_ctas_per_sm(int nb) { return nb == 1 ? 4 : 3; }
+constexpr int kDecCtasPerSm = 3;
 
 using AttnKernel = void (*)(AttnParams);
 
@@ -62,7 +62,7 @@ int kv_device(int* dev) {
   if (g_kv_set[*dev].load(std::memory_order_relaxed)) return SVDQ_OK;
   SVDQ_CUDA(cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (2 * kPlanMaxRequests + 1) * static_cast<int>(sizeof(int))));
-  if (g_dev[*dev].sms * 4 > kMaxAttnCtas) return SVDQ_ERR_CUDA;   // the workspace is laid out for 148 SMs
+  if (g_dev[*dev].sms * 3 > kMaxAttnCtas) return SVDQ_ERR_CUDA;   // the workspace is laid out for 148 SMs
   for (int fmt : {SVDQ_NVFP4, SVDQ_INT4, SVDQ_FP4G32})
     for (int D : {64, 128})
       for (int nb : {1, 2})
@@ -269,7 +269,7 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
       (d->table_width > 0 && d->block_table == nullptr) ||
       (d->rows > 1 && d->out_stride < static_cast<long long>(d->q_heads) * p.g.D))
     return SVDQ_ERR_INVALID_ARG;
-  if (d->batch > kAttnMaxBatch) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (d->batch > kAttnMaxBatch || static_cast<long long>(d->rows) * (d->q_heads / p.g.heads) > 0x7fff0000LL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (d->workspace == nullptr || (reinterpret_cast<uintptr_t>(d->workspace) & 255u)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
@@ -286,7 +286,7 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
   p.batch = d->batch;
   p.rows = d->rows;
   p.q_heads = d->q_heads;
-  p.rep = d->q_heads / p.g.heads;
+  p.rep = fast_div(d->q_heads / p.g.heads);
   p.causal = d->causal != 0;
   p.window = d->window;
   p.scale = d->scale;
@@ -297,10 +297,10 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
   p.min_units = 1;
   const int nb = dec_blocks(d);
   // enough CTAs for the most units that these rows and this table can hold
-  const long long tiles = std::min<long long>((static_cast<long long>(d->rows) * p.rep + 8 * nb - 1) / (8 * nb) + d->batch,
-                                              static_cast<long long>(d->rows) * p.rep);
+  const long long tiles = std::min<long long>((static_cast<long long>(d->rows) * p.rep.d + 8 * nb - 1) / (8 * nb) + d->batch,
+                                              static_cast<long long>(d->rows) * p.rep.d);
   const long long units = tiles * p.g.heads * std::max<long long>(1, ((static_cast<long long>(p.width) << p.g.page_log2) + kDecUnit - 1) / kDecUnit + 1);
-  const int ctas = static_cast<int>(std::min<long long>(units, static_cast<long long>(g_dev[dev].sms) * dec_ctas_per_sm(nb)));
+  const int ctas = static_cast<int>(std::min<long long>(units, static_cast<long long>(g_dev[dev].sms) * kDecCtasPerSm));
   SVDQ_CUDA(launch_pdl(dec_kernel(d->cache.fmt, p.g.D, nb), dim3(ctas), dim3(kDecThreads), dec_smem_bytes(d->cache.fmt, p.g.D, nb),
                        static_cast<cudaStream_t>(stream), 0u, p));
   return SVDQ_OK;

@@ -8,7 +8,7 @@
 // no key gives o = 0 and lse = -inf.
 //
 // This kernel is for few query rows per key head (decode): it reads the cache once
-// at the rate of HBM.  A warp takes 32 keys at a time, all D, from a ring of bulk
+// at the rate of HBM.  A warp takes 64 keys at a time, all D, from a ring of bulk
 // copies of its own, turns the codes into operand fragments in registers, and
 // keeps a running maximum and sum per row; the warps of a CTA take turns along the
 // keys and join at the end of an item.  The products run transposed,
@@ -42,16 +42,17 @@ namespace svdq {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecChunk = 32;                       // keys of a warp's step
+constexpr int kDecChunk = 64;                       // keys of a warp's step
+constexpr int kDecBlocks = kDecChunk / 16;
 constexpr int kDecUnit = kDecChunk * kDecWarps;     // keys of a unit of work
-constexpr int kDecStages = 3;
+constexpr int kDecStages = 2;
 
 __host__ __device__ constexpr int dec_stage_bytes(int fmt, int D) {
   return 2 * kDecChunk * (D / 2 + kv_scale_bytes(fmt, D));
 }
 __host__ __device__ constexpr uint32_t dec_smem_bytes(int fmt, int D, int NB) {
   return static_cast<uint32_t>(kDecWarps * kDecStages * dec_stage_bytes(fmt, D) + kDecWarps * kDecStages * 8 /* barriers */ +
-                               kDecWarps * kDecStages * 4 /* pieces */ + 2 * kDecWarps * 8 * NB * 4 /* max, sum */ + 128);
+                               kDecWarps * kDecStages * 4 /* blocks */ + 2 * kDecWarps * 8 * NB * 4 /* max, sum */ + 128);
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -255,7 +256,7 @@ __device__ __forceinline__ void key_scores(const uint8_t* codes, const uint8_t* 
 
 // O^T += V^T P^T for 16 keys.  w[nb][0..3]: the weights of this lane's score elements (keys of rows r and
 // r + 8, columns 2t and 2t + 1).  `usable`: keys below it are real, scales of the others count as zero.
-template <int FMT, int D, int NB>
+template <int FMT, int D, int NB, bool WHOLE>
 __device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* scales, int r, int t, int usable,
                                            const float (&w)[NB][4], float (&o)[NB][D / 16][4]) {
   int key[4];                                         // keys of contraction indices 2t, 2t + 1, 2t + 8, 2t + 9
@@ -265,8 +266,8 @@ __device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* 
     const int k0 = key_of_row(r), k1 = k0 + 8;
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
-      const float s0 = k0 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k0 * (D / 32) + 2 * g)) : 0.f;
-      const float s1 = k1 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k1 * (D / 32) + 2 * g)) : 0.f;
+      const float s0 = WHOLE || k0 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k0 * (D / 32) + 2 * g)) : 0.f;
+      const float s1 = WHOLE || k1 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k1 * (D / 32) + 2 * g)) : 0.f;
       uint32_t bh[NB][2], bl[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -325,7 +326,7 @@ __device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* 
       } else {
         c[i][0] = *reinterpret_cast<const uint32_t*>(at);
       }
-      sc[i] = key[i] < usable ? scales[key[i] * SB + g] : 0u;
+      sc[i] = WHOLE || key[i] < usable ? scales[key[i] * SB + g] : 0u;
     }
     const uint32_t s01 = e4m3x2_to_f16(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16(sc[2] | (sc[3] << 8));
 #pragma unroll
@@ -356,8 +357,90 @@ __device__ __forceinline__ int value_element(int r, int j) {
   return (D / 8) * r + 2 * j;
 }
 
+// Weights and values of one step: kDecBlocks blocks of 16 keys from `kc`.  WHOLE: every row sees every key.
+// `base` is the first key, `have` a bit per block that was loaded.
+template <int FMT, int D, int NB, bool WHOLE>
+__device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int base, int have, int limit, const uint32_t (&qf)[NB][D / 8],
+                                         const float (&factor)[NB][2], const int (&lo_key)[NB][2], const int (&hi_key)[NB][2],
+                                         float (&m)[NB][2], float (&l)[NB][2], float (&o)[NB][D / 16][4]) {
+  constexpr int SB = kv_scale_bytes(FMT, D);
+  const uint8_t* ks = kc + kDecChunk * (D / 2);
+  const uint8_t* vc = kc + kDecChunk * (D / 2 + SB);
+  const uint8_t* vs = vc + kDecChunk * (D / 2);
+  const int kr = key_of_row(r);
+  float s[kDecBlocks][NB][4];
+#pragma unroll
+  for (int u = 0; u < kDecBlocks; ++u) {
+    key_scores<FMT, D, NB>(kc + u * 16 * (D / 2), ks + u * 16 * SB, kr, t, qf, s[u]);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[u][nb][i] *= factor[nb][i & 1];
+        if (!WHOLE) {
+          const int key = base + 16 * u + kr + (i & 2 ? 8 : 0);
+          const bool see = ((have >> u) & 1) && key < limit && key < hi_key[nb][i & 1] && key >= lo_key[nb][i & 1];
+          if (!see) s[u][nb][i] = -INFINITY;
+        }
+      }
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    float top[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      top[j] = fmaxf(s[0][nb][j], s[0][nb][j + 2]);
+#pragma unroll
+      for (int u = 1; u < kDecBlocks; ++u) top[j] = fmax3(top[j], s[u][nb][j], s[u][nb][j + 2]);
+    }
+    // a lane whose own maximum passes the running one makes the warp look for the new one
+    if (__any_sync(0xffffffffu, top[0] > m[nb][0] || top[1] > m[nb][1])) {
+      float c2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], x));
+        const float m2 = fmaxf(m[nb][j], top[j]);
+        c2[j] = m2 == -INFINITY ? 1.f : ex2(m[nb][j] - m2);
+        m[nb][j] = m2;
+        l[nb][j] *= c2[j];
+      }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nb][d][i] *= c2[i & 1];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float sub = m[nb][j] == -INFINITY ? 0.f : m[nb][j] - 15.f;
+#pragma unroll
+      for (int u = 0; u < kDecBlocks; ++u)
+#pragma unroll
+        for (int i = j; i < 4; i += 2) {
+          s[u][nb][i] = ex2(s[u][nb][i] - sub);
+          l[nb][j] += s[u][nb][i];
+        }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kDecBlocks; ++u) {
+    const int usable = WHOLE ? 16 : (((have >> u) & 1) ? limit - base - 16 * u : 0);
+    add_values<FMT, D, NB, WHOLE>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, usable, s[u], o);
+  }
+}
+
+// Writes four elements of a finished row, and its lse.
+__device__ __forceinline__ void write_row(const AttnParams& p, int row0, int h, int row, int d, int D, float4 acc, float top, float sum) {
+  const int i = row / p.rep, hq = h * p.rep.d + row - i * p.rep.d;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint2*>(p.out + (row0 + i) * p.out_stride + hq * D + d) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse != nullptr && d == 0)
+    p.lse[static_cast<long long>(row0 + i) * p.q_heads + hq] = sum > 0.f ? (top - 15.f + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
 template <int FMT, int D, int NB>
-__global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const AttnParams p) {
   constexpr int RT = 8 * NB;
   constexpr int STAGE = dec_stage_bytes(FMT, D);
   constexpr int SB = kv_scale_bytes(FMT, D);
@@ -367,7 +450,7 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
   const int warp = static_cast<int>(warp_id()), lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   uint8_t* ring = dec_smem + warp * kDecStages * STAGE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(dec_smem + kDecWarps * kDecStages * STAGE) + warp * kDecStages;
-  int* pieces = reinterpret_cast<int*>(dec_smem + kDecWarps * kDecStages * (STAGE + 8)) + warp * kDecStages;
+  int* loaded = reinterpret_cast<int*>(dec_smem + kDecWarps * kDecStages * (STAGE + 8)) + warp * kDecStages;
   float* row_max = reinterpret_cast<float*>(dec_smem + kDecWarps * kDecStages * (STAGE + 12));   // [warps][RT]
   float* row_sum = row_max + kDecWarps * RT;
   __shared__ Share share;
@@ -384,12 +467,16 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
   int count = share.count;
   if (count == 0) return;
   int b = share.b, h = share.h, rt = share.rt, unit = share.unit;
-  const long long total = share.total, begin = share.begin;
-  const int ctas = share.ctas;
-  long long at = begin;                               // unit number of the current segment's first unit
+  long long at = share.begin;                         // unit number of the current segment's first unit
   Request req = load_request(p, b);
-  int it = 0;                                         // chunks that this warp has used so far
+  uint32_t phase = 0;                                 // bit s: parity of stage s
   bool dead = false;                                  // a wait ran out
+
+  // Pieces of a step that lie in one page are copied by lanes 0 .. pieces - 1.
+  const int piece_log2 = min(p.g.page_log2, 6);
+  static_assert(kDecChunk == 64, "the copies' steps");
+  const int piece = 1 << piece_log2;
+  const bool copier = (lane << piece_log2) < kDecChunk;
 
   while (true) {
     int k0, k1;
@@ -397,35 +484,78 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
     const int units = max(1, (k1 - k0 + kDecUnit - 1) / kDecUnit);
     const int here = min(units - unit, count);
     const int first = k0 + unit * kDecUnit;           // keys of this segment
-    const int limit = min(k1, here >= units - unit ? k1 : first + here * kDecUnit);
+    const int limit = here >= units - unit ? k1 : first + here * kDecUnit;
+    const int* table = p.table + b * p.table_stride;
+    int next = first + warp * kDecChunk;              // first key of the next step to be copied; kDecUnit apart
+    const int steps = limit > next ? (limit - next + kDecUnit - 1) / kDecUnit : 0;
+
+    // The page of this lane's piece of the step at `next`: -1 past the end, or outside the pool.
+    auto page_of = [&](int key0) {
+      const int key = key0 + (lane << piece_log2);
+      int page = -1;
+      if (copier && key < limit) {
+        page = table[key >> p.g.page_log2];
+        if (page >= p.g.num_pages) page = -2;
+        if (page < 0) raise_error(kErrIndex);
+      }
+      return page;
+    };
+    auto issue = [&](int st, int key0, int page) {
+      const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) {
+        // a bit per piece becomes a bit per 16 keys
+        const unsigned spread = piece_log2 == 4 ? good : piece_log2 == 5 ? (good & 1) * 3 + (good >> 1) * 12 : good * 15;
+        loaded[st] = static_cast<int>(spread);
+        mbar_arrive_expect_tx(&bars[st], (__popc(good) << piece_log2) * 2 * (D / 2 + SB));
+      }
+      __syncwarp();
+      if (page >= 0) {
+        const int k = lane << piece_log2, off = (key0 + k) & (p.g.page - 1);
+        const uint8_t* blk = p.g.pool + kv_block(p.g, page, h);
+        uint8_t* dst = ring + st * STAGE;
+        bulk_load(dst + k * (D / 2), blk + off * (D / 2), piece * (D / 2), &bars[st]);
+        bulk_load(dst + kDecChunk * (D / 2) + k * SB, blk + p.g.ks + off * SB, piece * SB, &bars[st]);
+        bulk_load(dst + STAGE / 2 + k * (D / 2), blk + p.g.vc + off * (D / 2), piece * (D / 2), &bars[st]);
+        bulk_load(dst + STAGE / 2 + kDecChunk * (D / 2) + k * SB, blk + p.g.vs + off * SB, piece * SB, &bars[st]);
+      }
+    };
+    int flying = 0;                                   // copies on their way
+    if (!dead) {
+      int pages[kDecStages];
+#pragma unroll
+      for (int s = 0; s < kDecStages; ++s) pages[s] = page_of(next + s * kDecUnit);
+#pragma unroll
+      for (int s = 0; s < kDecStages; ++s)
+        if (s < steps) {
+          issue(s, next, pages[s]);
+          next += kDecUnit;
+          ++flying;
+        }
+    }
 
     // this lane's score columns: rows 2t, 2t + 1 of each block
-    const long long rows = static_cast<long long>(req.n) * p.rep;
+    const int rows = req.n * p.rep.d;
     uint32_t qf[NB][D / 8];
     float factor[NB][2];
     int lo_key[NB][2], hi_key[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const long long row = static_cast<long long>(rt) * RT + nb * 8 + r;
+      const int row = rt * RT + nb * 8 + r;
       const bool live = row < rows;
-      const int i = live ? static_cast<int>(row / p.rep) : 0, hq = live ? h * p.rep + static_cast<int>(row % p.rep) : 0;
+      const int i = live ? row / p.rep : 0, hq = h * p.rep.d + (live ? row - i * p.rep.d : 0);
       float f;
       load_queries<FMT, D>(p.q + (req.row0 + i) * p.q_stride + hq * D, live, t, qf[nb], f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         factor[nb][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4) * (p.scale * 1.4426950408889634f);
-        const long long rj = static_cast<long long>(rt) * RT + nb * 8 + 2 * t + j;
-        const int ij = static_cast<int>(min(rj, rows - 1) / p.rep);
-        const int pos = req.kv - req.n + ij;
+        const int pos = req.kv - req.n + min(rt * RT + nb * 8 + 2 * t + j, rows - 1) / p.rep;
         hi_key[nb][j] = p.causal ? min(req.kv, pos + 1) : req.kv;
         lo_key[nb][j] = p.window > 0 ? pos - p.window + 1 : 0;
       }
     }
     // keys that every row of the tile sees
-    const int i_first = static_cast<int>(static_cast<long long>(rt) * RT / p.rep);
-    const int i_last = static_cast<int>((min((rt + 1LL) * RT, rows) - 1) / p.rep);
-    const int all_hi = p.causal ? min(req.kv, req.kv - req.n + i_first + 1) : req.kv;
-    const int all_lo = p.window > 0 ? req.kv - req.n + i_last - p.window + 1 : 0;
+    const int all_hi = min(limit, p.causal ? req.kv - req.n + (rt * RT) / p.rep + 1 : req.kv);
+    const int all_lo = p.window > 0 ? req.kv - req.n + (min((rt + 1) * RT, rows) - 1) / p.rep - p.window + 1 : 0;
 
     float m[NB][2], l[NB][2], o[NB][D / 16][4];
 #pragma unroll
@@ -441,137 +571,37 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
         for (int i = 0; i < 4; ++i) o[nb][d][i] = 0.f;
     }
 
-    const int* table = p.table + b * p.table_stride;
-    const int mine = first + warp * kDecChunk;        // this warp's first chunk; the next is kDecUnit on
-    const int chunks = limit > mine ? (limit - mine + kDecUnit - 1) / kDecUnit : 0;
-
-    // Copies of the chunk `c` into stage (it + c) % kDecStages: lane 0 (and lane 1 with pages of 16) each
-    // bring the part that lies in one page; a part at or past `limit` or in a bad page is left out.
-    const int piece = p.g.page >= kDecChunk ? kDecChunk : 16;
-    const bool copier = lane * piece < kDecChunk;
-    auto page_of = [&](int c) {
-      const long long key = static_cast<long long>(mine) + static_cast<long long>(c) * kDecUnit + lane * piece;
-      if (!copier || c >= chunks || key >= limit) return -1;
-      const int page = table[key >> p.g.page_log2];
-      if (page < 0 || page >= p.g.num_pages) {
-        raise_error(kErrIndex);
-        return -1;
+    int base = first + warp * kDecChunk;
+    int st = 0;
+    for (int left = dead ? 0 : steps; left > 0; --left) {
+      const int page = page_of(next);                 // looked up a step ahead of its copy
+      if (!warp_wait(&bars[st], (phase >> st) & 1, p.budget, nullptr)) {
+        if (lane == 0) raise_error(kErrWaitAttn);
+        dead = true;                                  // copies in flight land before the ring is given up
+        for (; flying > 0; --flying) {
+          warp_wait(&bars[st], (phase >> st) & 1, drain_budget(p.budget), nullptr);
+          phase ^= 1u << st;
+          st = st + 1 == kDecStages ? 0 : st + 1;
+        }
+        break;
       }
-      return page;
-    };
-    auto issue = [&](int c, int page) {
-      const int st = (it + c) % kDecStages;
-      const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
-      constexpr int kPieceBytes16 = 2 * 16 * (D / 2 + SB);
-      if (lane == 0) {
-        pieces[st] = piece == kDecChunk ? ((good & 1) ? 3 : 0) : static_cast<int>(good & 3);
-        mbar_arrive_expect_tx(&bars[st], __popc(good) * (piece / 16) * kPieceBytes16);
+      const uint8_t* kc = ring + st * STAGE;
+      const int have = loaded[st];
+      if (have == (1 << kDecBlocks) - 1 && base >= all_lo && base + kDecChunk <= all_hi)
+        dec_step<FMT, D, NB, true>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o);
+      else
+        dec_step<FMT, D, NB, false>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o);
+      phase ^= 1u << st;
+      --flying;
+      __syncwarp();                                   // every lane has left the stage
+      if (left > kDecStages) {
+        issue(st, next, page);
+        next += kDecUnit;
+        ++flying;
       }
-      __syncwarp();
-      if (page >= 0) {
-        const int key = mine + c * kDecUnit + lane * piece;
-        const int off = key & (p.g.page - 1);
-        const uint8_t* blk = p.g.pool + kv_block(p.g, page, h);
-        uint8_t* dst = ring + st * STAGE;
-        const int k = lane * piece;
-        bulk_load(dst + k * (D / 2), blk + off * (D / 2), piece * (D / 2), &bars[st]);
-        bulk_load(dst + kDecChunk * (D / 2) + k * SB, blk + p.g.ks + off * SB, piece * SB, &bars[st]);
-        bulk_load(dst + STAGE / 2 + k * (D / 2), blk + p.g.vc + off * (D / 2), piece * (D / 2), &bars[st]);
-        bulk_load(dst + STAGE / 2 + kDecChunk * (D / 2) + k * SB, blk + p.g.vs + off * SB, piece * SB, &bars[st]);
-      }
-    };
-    if (!dead) {
-      for (int c = 0; c < min(chunks, kDecStages - 1); ++c) issue(c, page_of(c));
-      int page = page_of(kDecStages - 1);
-      int issued = min(chunks, kDecStages - 1);
-      for (int c = 0; c < chunks; ++c) {
-        __syncwarp();                                 // every lane has left the stage that is filled next
-        if (c + kDecStages - 1 < chunks) {
-          issue(c + kDecStages - 1, page);
-          ++issued;
-        }
-        page = page_of(c + kDecStages);               // looked up a step ahead of its copy
-        const int st = (it + c) % kDecStages;
-        if (!warp_wait(&bars[st], ((it + c) / kDecStages) & 1, p.budget, nullptr)) {
-          if (lane == 0) raise_error(kErrWaitAttn);
-          dead = true;
-          for (; c < issued; ++c)                     // copies in flight land before the ring is given up
-            warp_wait(&bars[(it + c) % kDecStages], ((it + c) / kDecStages) & 1, drain_budget(p.budget), nullptr);
-          break;
-        }
-        const uint8_t* kc = ring + st * STAGE;
-        const uint8_t* vc = kc + STAGE / 2;
-        const uint8_t* ks = kc + kDecChunk * (D / 2);
-        const uint8_t* vs = vc + kDecChunk * (D / 2);
-        const int base = mine + c * kDecUnit;
-        const int have = pieces[st];
-        float s[2][NB][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) key_scores<FMT, D, NB>(kc + u * 16 * (D / 2), ks + u * 16 * SB, key_of_row(r), t, qf, s[u]);
-        const bool whole = have == 3 && base >= all_lo && base + kDecChunk <= all_hi && base + kDecChunk <= limit;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[u][nb][i] *= factor[nb][i & 1];
-        if (!whole) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int key = base + 16 * u + key_of_row(r) + (i & 2 ? 8 : 0);
-                const bool see = ((have >> u) & 1) && key < limit && key < hi_key[nb][i & 1] && key >= lo_key[nb][i & 1];
-                if (!see) s[u][nb][i] = -INFINITY;
-              }
-        }
-        // maximum of each column over the chunk, then weights
-        float w[2][NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float top[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            top[j] = fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
-#pragma unroll
-            for (int x = 4; x < 32; x *= 2) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], x));
-          }
-          if (__any_sync(0xffffffffu, top[0] > m[nb][0] || top[1] > m[nb][1])) {
-            float c2[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float m2 = fmaxf(m[nb][j], top[j]);
-              c2[j] = m2 == -INFINITY ? 1.f : ex2(m[nb][j] - m2);
-              m[nb][j] = m2;
-              l[nb][j] *= c2[j];
-            }
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[nb][d][i] *= c2[i & 1];
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float sub = m[nb][j] == -INFINITY ? 0.f : m[nb][j] - 15.f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int i = j; i < 4; i += 2) {
-                w[u][nb][i] = ex2(s[u][nb][i] - sub);
-                l[nb][j] += w[u][nb][i];
-              }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int usable = whole ? 16 : (((have >> u) & 1) ? limit - base - 16 * u : 0);
-          add_values<FMT, D, NB>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, usable, w[u], o);
-        }
-      }
+      base += kDecUnit;
+      st = st + 1 == kDecStages ? 0 : st + 1;
     }
-    it += chunks;
 
     // ------------------------------------------------ join the warps of the CTA
 #pragma unroll
@@ -602,13 +632,13 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
               make_float2(o[nb][d][j] * c, o[nb][d][j + 2] * c);
       }
     __syncthreads();
-    const int live_rows = static_cast<int>(min(static_cast<long long>(RT), rows - static_cast<long long>(rt) * RT));
+    const int live_rows = min(RT, rows - rt * RT);
     const bool split = unit > 0 || here < units;
-    const long long item = at - unit;                 // unit number of the item's first unit
     constexpr int Q = D / 4;
+    constexpr int SLOT = RT * (D + 2);
     const float* all = reinterpret_cast<const float*>(dec_smem);
     constexpr int kWarpFloats = kDecStages * STAGE / 4;
-    float* slot = p.partials + (2ll * blockIdx.x + (at == begin ? 0 : 1)) * (RT * (D + 2));
+    float* slot = p.partials + (2ll * blockIdx.x + (at == share.begin ? 0 : 1)) * SLOT;
     for (int e = threadIdx.x; e < live_rows * Q; e += kDecThreads) {
       const int row = e / Q, d = e % Q * 4;
       float top = row_max[row];
@@ -624,21 +654,15 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
       }
       if (!split) {
-        const long long gr = static_cast<long long>(rt) * RT + row;
-        const int i = static_cast<int>(gr / p.rep), hq = h * p.rep + static_cast<int>(gr % p.rep);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        *reinterpret_cast<uint2*>(p.out + (req.row0 + i) * p.out_stride + hq * D + d) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (p.lse != nullptr && d == 0)
-          p.lse[static_cast<long long>(req.row0 + i) * p.q_heads + hq] =
-              sum > 0.f ? (top - 15.f + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        write_row(p, req.row0, h, rt * RT + row, d, D, acc, top, sum);
       } else {
         __stcg(reinterpret_cast<float4*>(slot + row * D + d), acc);
         if (d == 0) __stcg(reinterpret_cast<float2*>(slot + RT * D + 2 * row), make_float2(top, sum));
       }
     }
     if (split) {
-      const int c0 = share_of(total, ctas, item), c1 = share_of(total, ctas, item + units - 1);
+      const long long item = at - unit;               // unit number of the item's first unit
+      const int c0 = share_of(share.base, share.rem, item), c1 = share_of(share.base, share.rem, item + units - 1);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -647,32 +671,24 @@ __global__ void __launch_bounds__(kDecThreads, NB == 1 ? 4 : 3) kv_attn_decode_k
       }
       __syncthreads();
       if (last_flag) {
-        const int slot0 = share_begin(total, ctas, c0) == item ? 2 * c0 : 2 * c0 + 1;
+        const float* part0 = p.partials + (share_begin(share.base, share.rem, c0) == item ? 2ll * c0 : 2ll * c0 + 1) * SLOT;
         for (int e = threadIdx.x; e < live_rows * Q; e += kDecThreads) {
           const int row = e / Q, d = e % Q * 4;
-          float top = -INFINITY;
-          for (int c = c0; c <= c1; ++c) {
-            const float* sl = p.partials + static_cast<long long>(c == c0 ? slot0 : 2 * c) * (RT * (D + 2));
-            top = fmaxf(top, __ldcg(sl + RT * D + 2 * row));
-          }
-          float sum = 0.f;
+          float top = -INFINITY, sum = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
           for (int c = c0; c <= c1; ++c) {
-            const float* sl = p.partials + static_cast<long long>(c == c0 ? slot0 : 2 * c) * (RT * (D + 2));
+            const float* sl = c == c0 ? part0 : p.partials + 2ll * c * SLOT;
             const float2 ms = __ldcg(reinterpret_cast<const float2*>(sl + RT * D + 2 * row));
-            const float f = ms.x == -INFINITY ? 0.f : ex2(ms.x - top);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + row * D + d));
-            sum = fmaf(ms.y, f, sum);
-            acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+            const float m2 = fmaxf(top, ms.x);
+            const float f0 = m2 == -INFINITY ? 0.f : ex2(top - m2), f1 = m2 == -INFINITY ? 0.f : ex2(ms.x - m2);
+            sum = sum * f0 + ms.y * f1;
+            acc.x = acc.x * f0 + v.x * f1, acc.y = acc.y * f0 + v.y * f1;
+            acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
+            top = m2;
           }
-          const long long gr = static_cast<long long>(rt) * RT + row;
-          const int i = static_cast<int>(gr / p.rep), hq = h * p.rep + static_cast<int>(gr % p.rep);
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
-          *reinterpret_cast<uint2*>(p.out + (req.row0 + i) * p.out_stride + hq * D + d) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-          if (p.lse != nullptr && d == 0)
-            p.lse[static_cast<long long>(req.row0 + i) * p.q_heads + hq] =
-                sum > 0.f ? (top - 15.f + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          write_row(p, req.row0, h, rt * RT + row, d, D, acc, top, sum);
         }
       }
     }

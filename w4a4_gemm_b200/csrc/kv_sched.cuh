@@ -18,6 +18,25 @@
 
 namespace svdq {
 
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): m = ceil(2^(31 + s) / d), s = ceil(log2 d).
+struct FastDiv {
+  uint32_t m;
+  int shift, d;
+};
+__host__ inline FastDiv fast_div(int d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  FastDiv f;
+  f.d = d;
+  f.shift = 31 + s;
+  f.m = static_cast<uint32_t>(((1ull << f.shift) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ int operator/(int n, const FastDiv& f) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(n)) * f.m) >> f.shift);
+}
+
 struct AttnParams {
   KvGeom g;
   const __nv_bfloat16* q;
@@ -30,7 +49,8 @@ struct AttnParams {
   const int* table;
   long long table_stride;
   int width;
-  int batch, rows, q_heads, rep; // rep: query heads per key head
+  int batch, rows, q_heads;
+  FastDiv rep;                   // query heads per key head; rows * rep < 2^31
   int causal, window;
   float scale;
   float* partials;               // workspace: 2 slots per CTA of RT x D sums and RT (max, sum) pairs
@@ -59,11 +79,9 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
 // Keys [k0, k1) that any row of tile rt sees; k0 is cut down to a multiple of KT.
 template <int RT, int KT>
 __device__ __forceinline__ void tile_keys(const AttnParams& p, const Request& r, int rt, int& k0, int& k1) {
-  const long long rows = static_cast<long long>(r.n) * p.rep;
-  const int i0 = static_cast<int>(static_cast<long long>(rt) * RT / p.rep);
-  const int i1 = static_cast<int>((min((rt + 1LL) * RT, rows) - 1) / p.rep);
-  k1 = p.causal ? max(0, min(r.kv, r.kv - r.n + i1 + 1)) : r.kv;
-  k0 = p.window > 0 ? max(0, r.kv - r.n + i0 - p.window + 1) : 0;
+  const int rows = r.n * p.rep.d;
+  k1 = p.causal ? max(0, min(r.kv, r.kv - r.n + (min((rt + 1) * RT, rows) - 1) / p.rep + 1)) : r.kv;
+  k0 = p.window > 0 ? max(0, r.kv - r.n + (rt * RT) / p.rep - p.window + 1) : 0;
   k0 = min(k0, k1) / KT * KT;
 }
 
@@ -77,7 +95,7 @@ __device__ __forceinline__ int tile_units(const AttnParams& p, const Request& r,
 
 template <int RT>
 __device__ __forceinline__ int row_tiles(const AttnParams& p, const Request& r) {
-  return static_cast<int>((static_cast<long long>(r.n) * p.rep + RT - 1) / RT);
+  return (r.n * p.rep.d + RT - 1) / RT;
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -127,21 +145,23 @@ __device__ __forceinline__ long long warp_inclusive(long long v) {
 
 // Where a CTA's share begins, and its size.  In shared memory.
 struct Share {
-  long long total;               // units of the whole launch
+  long long base;                // units of a CTA's share; the first `rem` CTAs have one more
   long long begin;               // first unit of this CTA
-  int ctas;                      // CTAs that have a share
+  int rem;
   int count;                     // units of this CTA (0: none)
   int b, h, rt, unit;            // the item of the first unit, and the unit inside it
 };
 
-__host__ __device__ inline long long share_begin(long long total, int ctas, int c) { return total * c / ctas; }
-
+// n / d, in 32 bits where they hold it (the usual case; 64-bit division is a long subroutine).
+__device__ __forceinline__ long long div_units(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+  return n / d;
+}
+__device__ __forceinline__ long long share_begin(long long base, int rem, int c) { return base * c + min(c, rem); }
 // The CTA whose share holds unit u.
-__device__ __forceinline__ int share_of(long long total, int ctas, long long u) {
-  int c = static_cast<int>(u * ctas / total);
-  while (share_begin(total, ctas, c + 1) <= u) ++c;
-  while (share_begin(total, ctas, c) > u) --c;
-  return c;
+__device__ __forceinline__ int share_of(long long base, int rem, long long u) {
+  const long long head = (base + 1) * rem;
+  return static_cast<int>(u < head ? div_units(u, base + 1) : rem + div_units(u - head, base));
 }
 
 // Called by all threads.  `sums` holds (batch + 31) / 32 words of shared memory.
@@ -150,39 +170,46 @@ __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (p.batch + 31) / 32;
   Request r;
+  long long one = 0;                          // units of one key head of this lane's request
   for (int g = warp; g < groups; g += warps) {
-    const long long t = warp_sum(group_units<RT, KT>(p, 32 * g, r));
+    one = group_units<RT, KT>(p, 32 * g, r);
+    const long long t = warp_sum(one);
     if (lane == 0) sums[g] = t * p.g.heads;
   }
-  __syncthreads();
+  if (groups > 1) __syncthreads();
   if (warp == 0) {
+    __syncwarp();
     long long total = 0;
     for (int g = lane; g < groups; g += 32) total += sums[g];
     total = warp_sum(total);
-    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + p.min_units - 1) / p.min_units));
+    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), div_units(total + p.min_units - 1, p.min_units)));
     const int c = blockIdx.x;
     if (c >= ctas) {                          // also when there is no work at all
       if (lane == 0) s->count = 0;
     } else {
-      const long long begin = share_begin(total, ctas, c), end = share_begin(total, ctas, c + 1);
-      // the group of 32 requests that holds `begin`
+      const long long each = div_units(total, ctas);
+      const int rem = static_cast<int>(total - each * ctas);
+      const long long begin = share_begin(each, rem, c), end = share_begin(each, rem, c + 1);
       long long left = begin;
       int g = 0;
-      for (int base = 0;; base += 32) {
-        const long long v = base + lane < groups ? sums[base + lane] : 0;
-        const long long inc = warp_inclusive(v);
-        const unsigned over = __ballot_sync(0xffffffffu, inc > left);
-        if (over) {
-          const int k = __ffs(over) - 1;
-          left -= __shfl_sync(0xffffffffu, inc - v, k);
-          g = base + k;
-          break;
+      if (groups > 1) {
+        // the group of 32 requests that holds `begin`
+        for (int base = 0;; base += 32) {
+          const long long v = base + lane < groups ? sums[base + lane] : 0;
+          const long long inc = warp_inclusive(v);
+          const unsigned over = __ballot_sync(0xffffffffu, inc > left);
+          if (over) {
+            const int k = __ffs(over) - 1;
+            left -= __shfl_sync(0xffffffffu, inc - v, k);
+            g = base + k;
+            break;
+          }
+          left -= __shfl_sync(0xffffffffu, inc, 31);
+          if (base + 32 >= groups) break;     // not reached: begin < total
         }
-        left -= __shfl_sync(0xffffffffu, inc, 31);
-        if (base + 32 >= groups) break;       // not reached: begin < total
+        one = group_units<RT, KT>(p, 32 * g, r);
       }
       // the request, the key head, the row tile
-      const long long one = group_units<RT, KT>(p, 32 * g, r);
       const long long v = one * p.g.heads, inc = warp_inclusive(v);
       const unsigned over = __ballot_sync(0xffffffffu, inc > left);
       const int k = over ? __ffs(over) - 1 : 0;
@@ -192,26 +219,28 @@ __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums,
       o.row0 = 0;
       o.n = __shfl_sync(0xffffffffu, r.n, k);
       o.kv = __shfl_sync(0xffffffffu, r.kv, k);
-      const int h = static_cast<int>(left / per_head);
+      const int h = static_cast<int>(div_units(left, per_head));
       left -= h * per_head;
       const int tiles = row_tiles<RT>(p, o);
       int rt = 0;
-      for (int base = 0; base < tiles; base += 32) {
-        const long long w = base + lane < tiles ? tile_units<RT, KT>(p, o, base + lane) : 0;
-        const long long winc = warp_inclusive(w);
-        const unsigned past = __ballot_sync(0xffffffffu, winc > left);
-        if (past) {
-          const int j = __ffs(past) - 1;
-          left -= __shfl_sync(0xffffffffu, winc - w, j);
-          rt = base + j;
-          break;
+      if (tiles > 1) {
+        for (int base = 0; base < tiles; base += 32) {
+          const long long w = base + lane < tiles ? tile_units<RT, KT>(p, o, base + lane) : 0;
+          const long long winc = warp_inclusive(w);
+          const unsigned past = __ballot_sync(0xffffffffu, winc > left);
+          if (past) {
+            const int j = __ffs(past) - 1;
+            left -= __shfl_sync(0xffffffffu, winc - w, j);
+            rt = base + j;
+            break;
+          }
+          left -= __shfl_sync(0xffffffffu, winc, 31);
         }
-        left -= __shfl_sync(0xffffffffu, winc, 31);
       }
       if (lane == 0) {
-        s->total = total;
+        s->base = each;
         s->begin = begin;
-        s->ctas = ctas;
+        s->rem = rem;
         s->count = static_cast<int>(min(end - begin, 0x7fffffffLL));
         s->b = 32 * g + k;
         s->h = h;
@@ -233,12 +262,11 @@ __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums,
 
 // One thread.  True if this is the last of `parts` arrivals.
 __device__ __forceinline__ bool arrive_last(unsigned long long* word, unsigned long long nonce, int parts) {
-  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  unsigned long long old = 0;                 // what a workspace in use holds between launches
   while (true) {
     const unsigned long long count = (old & ~0xFFFFull) == nonce ? (old & 0xFFFFull) : 0ull;
     const bool last = count + 1 == static_cast<unsigned long long>(parts);
-    const unsigned long long now = last ? 0ull : (nonce | (count + 1));
-    const unsigned long long seen = atomicCAS(word, old, now);
+    const unsigned long long seen = atomicCAS(word, old, last ? 0ull : (nonce | (count + 1)));
     if (seen == old) return last;
     old = seen;
   }
