@@ -5,6 +5,7 @@
 #pragma once
 
 #include "kv_attn.cuh"
+#include "kv_attn_rows.cuh"
 #include "kv_cache.cuh"
 #include "kv_plan.cuh"
 #include "qk_norm_rope.cuh"
@@ -29,6 +30,12 @@ int dec_blocks(const svdq_kv_attention_desc* d) {
 }
 constexpr int kDecCtasPerSm = 3;
 
+// The tcgen05 kernel takes the call where a key head has more than this many query rows per request.
+constexpr int kRowsFrom = 32;
+bool many_rows(const svdq_kv_attention_desc* d) {
+  return d->batch > 0 && static_cast<long long>(d->rows) * (d->q_heads / d->cache.kv_heads) > static_cast<long long>(kRowsFrom) * d->batch;
+}
+
 using AttnKernel = void (*)(AttnParams);
 
 template <int FMT>
@@ -38,6 +45,15 @@ AttnKernel dec_kernel_of(int D, int nb) {
 }
 AttnKernel dec_kernel(int fmt, int D, int nb) {
   return fmt == SVDQ_NVFP4 ? dec_kernel_of<kFmtNvfp4>(D, nb) : fmt == SVDQ_INT4 ? dec_kernel_of<kFmtInt4>(D, nb) : dec_kernel_of<kFmtFp4g32>(D, nb);
+}
+
+template <int FMT>
+AttnKernel rows_kernel_of(int D, int* smem) {
+  *smem = D == 64 ? RowsSmem<FMT, 64>::kBytes : RowsSmem<FMT, 128>::kBytes;
+  return D == 64 ? kv_attn_rows_kernel<FMT, 64> : kv_attn_rows_kernel<FMT, 128>;
+}
+AttnKernel rows_kernel(int fmt, int D, int* smem) {
+  return fmt == SVDQ_NVFP4 ? rows_kernel_of<kFmtNvfp4>(D, smem) : fmt == SVDQ_INT4 ? rows_kernel_of<kFmtInt4>(D, smem) : rows_kernel_of<kFmtFp4g32>(D, smem);
 }
 
 // 48 bits that differ from launch to launch (a counter spread by an odd multiplier and
@@ -68,6 +84,16 @@ int kv_device(int* dev) {
       for (int nb : {1, 2})
         SVDQ_CUDA(cudaFuncSetAttribute(dec_kernel(fmt, D, nb), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(dec_smem_bytes(fmt, D, nb))));
+  for (int fmt : {SVDQ_NVFP4, SVDQ_INT4, SVDQ_FP4G32})
+    for (int D : {64, 128}) {
+      int smem = 0;
+      AttnKernel k = rows_kernel(fmt, D, &smem);
+      SVDQ_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      cudaFuncAttributes at;
+      SVDQ_CUDA(cudaFuncGetAttributes(&at, k));
+      // its warp groups raise their registers to 184 out of what the block starts with: all of 65536, or they would wait
+      if (at.numRegs * kRowsThreads < 2 * 128 * 184 + 128 * 104 + 128 * 40) return SVDQ_ERR_CUDA;
+    }
   g_kv_set[*dev].store(true, std::memory_order_release);
   return SVDQ_OK;
 }
@@ -252,7 +278,9 @@ SVDQ_API int svdq_kv_attention_workspace_bytes(const svdq_kv_attention_desc* d, 
   const int rc = kv_geometry(&d->cache, &g, false);
   if (rc) return rc;
   if (d->q_heads < 1 || d->q_heads % g.heads != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  *bytes = kAttnCounterBytes + static_cast<size_t>(kMaxAttnCtas) * 2 * 8 * dec_blocks(d) * (g.D + 2) * sizeof(float);
+  const size_t rows = many_rows(d) ? static_cast<size_t>(kMaxAttnCtas / 3) * 2 * kRowsTile * (g.D + 2) * sizeof(float) : 0;
+  const size_t few = static_cast<size_t>(kMaxAttnCtas) * 2 * 8 * dec_blocks(d) * (g.D + 2) * sizeof(float);
+  *bytes = kAttnCounterBytes + std::max(rows, few);
   return SVDQ_OK;
 }
 
@@ -295,14 +323,21 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
   p.counters = static_cast<unsigned long long*>(d->workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(d->workspace) + kAttnCounterBytes);
   p.min_units = 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (many_rows(d)) {
+    p.min_units = 2;
+    int smem = 0;
+    AttnKernel k = rows_kernel(d->cache.fmt, p.g.D, &smem);
+    SVDQ_CUDA(launch_pdl(k, dim3(g_dev[dev].sms), dim3(kRowsThreads), static_cast<size_t>(smem), st, 0u, p));
+    return SVDQ_OK;
+  }
   const int nb = dec_blocks(d);
   // enough CTAs for the most units that these rows and this table can hold
   const long long tiles = std::min<long long>((static_cast<long long>(d->rows) * p.rep.d + 8 * nb - 1) / (8 * nb) + d->batch,
                                               static_cast<long long>(d->rows) * p.rep.d);
   const long long units = tiles * p.g.heads * std::max<long long>(1, ((static_cast<long long>(p.width) << p.g.page_log2) + kDecUnit - 1) / kDecUnit + 1);
   const int ctas = static_cast<int>(std::min<long long>(units, static_cast<long long>(g_dev[dev].sms) * kDecCtasPerSm));
-  SVDQ_CUDA(launch_pdl(dec_kernel(d->cache.fmt, p.g.D, nb), dim3(ctas), dim3(kDecThreads), dec_smem_bytes(d->cache.fmt, p.g.D, nb),
-                       static_cast<cudaStream_t>(stream), 0u, p));
+  SVDQ_CUDA(launch_pdl(dec_kernel(d->cache.fmt, p.g.D, nb), dim3(ctas), dim3(kDecThreads), dec_smem_bytes(d->cache.fmt, p.g.D, nb), st, 0u, p));
   return SVDQ_OK;
 }
 

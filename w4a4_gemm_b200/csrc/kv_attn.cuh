@@ -7,7 +7,7 @@
 // window t > pos_i - window, where pos_i = kv_len - q_len + i.  A query that sees
 // no key gives o = 0 and lse = -inf.
 //
-// This kernel is for few query rows per key head (decode): it reads the cache once
+// The kernel of this file is for few query rows per key head (decode): it reads the cache once
 // at the rate of HBM.  A warp takes 64 keys at a time, all D, from a ring of bulk
 // copies of its own, turns the codes into operand fragments in registers, and
 // keeps a running maximum and sum per row; the warps of a CTA take turns along the

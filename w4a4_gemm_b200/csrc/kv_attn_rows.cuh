@@ -1,0 +1,721 @@
+// kv_attn_rows.cuh -- attention over the paged 4-bit cache for many query rows
+// per key head (prompts, chunks of prompts, whole images), on tcgen05.
+//
+// A tile is 256 rows (a row is a token and one query head of the key head's
+// group) as two halves of 128, walked over the keys 128 at a time:
+//   S_w = Q_w K^T   (128 x 128 x D, operands in shared memory, TMEM columns 128 w)
+//   P_w = exp2(S_w f - m), fp16, written over S_w in TMEM
+//   O_w += P_w V    (128 x D x 128, P from TMEM, V from shared memory, columns 256 + 128 w)
+// Sixteen warps: two groups of four keep the softmax of a half each (a thread per
+// row: maximum, sum and row factor are private to it), four turn codes into fp16
+// tiles, one issues the MMAs.  While a half's softmax runs, the tensor core works
+// for the other half.
+//
+// Numbers.  FP4 values (code * scale) are exact in fp16.  INT4 values need up to 14
+// bits: keys enter as a pair hi + lo of fp16 values (exact to 2^-22, two MMAs),
+// values are rounded once to fp16 (2^-11, below the weights' own rounding); both are
+// divided by a power of two (the tile's largest key scale, the largest value scale so
+// far), which goes into the scores' factor and the sums' scale.  Queries are divided
+// by a power of two per row, as in the decode kernel.  The maximum is followed
+// lazily: it moves when a row's scores pass it by more than 2^5, so most tiles leave O
+// alone; weights are exp2(x - m + 10) <= 2^15 and keep 2^-11 relative down to
+// 2^-24 of the largest, 2^-35 absolute.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "kv_attn.cuh"
+#include "kv_cache.cuh"
+#include "kv_sched.cuh"
+#include "svdq_ptx.cuh"
+
+namespace svdq {
+
+constexpr int kRowsThreads = 512;
+constexpr int kRowsTile = 256;
+constexpr int kRowsKeys = 128;
+constexpr int kRowsRing = 4;                        // tiles whose masks and exponents are kept
+constexpr float kRowsLazy = 5.f, kRowsShift = 10.f;
+
+// Shared memory: Q (two halves), K stages (hi, and lo for INT4), V stages.
+template <int FMT, int D>
+struct RowsSmem {
+  static constexpr int kPanel = 128 * 128;          // 128 rows of 64 fp16 values, 128-byte swizzle
+  static constexpr int kTile = kPanel * (D / 64);
+  static constexpr int kParts = FMT == kFmtInt4 ? 2 : 1;
+  static constexpr int kKStages = (FMT == kFmtInt4 && D == 128) ? 1 : 2;
+  static constexpr int kVStages = 2;
+  static constexpr int kQ = 0;
+  static constexpr int kK = 2 * kTile;
+  static constexpr int kV = kK + kKStages * kParts * kTile;
+  static constexpr int kBars = kV + kVStages * kTile;
+  static constexpr int kMisc = kBars + 256;
+  static constexpr int kBytes = kMisc + 512 + 1024 /* alignment */;
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[smem] * B[smem], fp16 -> fp32; and with A in TMEM.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, P;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// fp16 x fp16 -> fp32; B K-major, or (transposed) with its N side contiguous.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_transposed) {
+  return (1u << 4) | (b_transposed ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Byte offset of 16-byte chunk c (8 values) of row r in a tile of 64-value panels.
+__device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
+  return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  unsigned long long x, y, z, w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(w));
+  return r;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long x, y, w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(w));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// A CTA's walk over the items of its share; every role keeps its own.
+struct Walk {
+  int b, h, rt, unit, count;
+  long long at;                  // unit number of the segment's first unit
+  Request req;
+  int k0, k1, units, here, first;
+};
+template <int RT, int KT>
+__device__ __forceinline__ void walk_segment(const AttnParams& p, Walk& w) {
+  tile_keys<RT, KT>(p, w.req, w.rt, w.k0, w.k1);
+  w.units = max(1, (w.k1 - w.k0 + KT - 1) / KT);
+  w.here = min(w.units - w.unit, w.count);
+  w.first = w.k0 + w.unit * KT;
+}
+template <int RT, int KT>
+__device__ __forceinline__ Walk walk_start(const AttnParams& p, const Share& s) {
+  Walk w;
+  w.b = s.b, w.h = s.h, w.rt = s.rt, w.unit = s.unit, w.count = s.count, w.at = s.begin;
+  if (w.count > 0) {
+    w.req = load_request(p, w.b);
+    walk_segment<RT, KT>(p, w);
+  }
+  return w;
+}
+// To the next item; false at the end of the share.
+template <int RT, int KT>
+__device__ __forceinline__ bool walk_next(const AttnParams& p, Walk& w) {
+  w.count -= w.here;
+  w.at += w.here;
+  if (w.count <= 0) return false;
+  w.unit = 0;
+  if (++w.rt >= row_tiles<RT>(p, w.req)) {
+    w.rt = 0;
+    if (++w.h >= p.g.heads) {
+      w.h = 0;
+      do {
+        if (++w.b >= p.batch) return false;         // not reached: the share ends inside the batch
+        w.req = load_request(p, w.b);
+      } while (w.req.n == 0);
+    }
+  }
+  walk_segment<RT, KT>(p, w);
+  return true;
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const AttnParams p) {
+  using L = RowsSmem<FMT, D>;
+  constexpr int RT = kRowsTile, KT = kRowsKeys;
+  constexpr int SB = kv_scale_bytes(FMT, D);
+  constexpr int SLOT = RT * (D + 2);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* q_full = bars;                            // [2] softmax -> MMA
+  uint64_t* s_full = bars + 2;                        // [2] MMA -> softmax
+  uint64_t* p_full = bars + 4;                        // [2] softmax -> MMA
+  uint64_t* o_full = bars + 6;                        // [2] MMA -> softmax, last tile of a segment
+  uint64_t* k_full = bars + 8;                        // [2] codes -> MMA
+  uint64_t* k_empty = bars + 10;                      // [2]
+  uint64_t* v_full = bars + 12;                       // [2]
+  uint64_t* v_empty = bars + 14;                      // [2]
+  uint64_t* join = bars + 16;                         // [2] the warps of a half, at a split item
+  uint64_t* exps = bars + 18;                         // the code warps, at a tile's exponents (INT4)
+  uint64_t* mma_done = bars + 19;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 20);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + L::kMisc);        // [ring][4]: a bit per key of a tile that counts
+  int* kexp = reinterpret_cast<int*>(masks + 4 * kRowsRing);             // [ring]
+  int* vexp = kexp + kRowsRing;                                          // [ring]
+  int* last_flag = vexp + kRowsRing;                                     // [2]
+  int* scratch = last_flag + 2;                                          // [2][8]
+  __shared__ Share share;
+  const int warp = static_cast<int>(warp_id()), lane = threadIdx.x & 31;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&join[i], 4);
+    }
+    mbar_init(exps, 4);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  find_share<RT, KT>(p, reinterpret_cast<long long*>(smem), &share);
+  fence_proxy_async_smem();                           // the scan's words lie under Q
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const long long budget = p.budget;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (warp_wait(bar, parity, budget, const_cast<int*>(abort_flag))) return true;
+    if (lane == 0) {
+      if (!*abort_flag) raise_error(kErrWaitAttn);
+      *abort_flag = 1;
+    }
+    return false;
+  };
+  // A barrier of the warps that arrive on `bar`, bounded like every other wait.
+  auto meet = [&](uint64_t* bar, uint32_t parity) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    return wait(bar, parity);
+  };
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int half = warp >> 2;
+    const int lrow = (warp & 3) * 32 + lane;          // row of the half = TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);   // lanes 32 (warp % 4) ..
+    const uint32_t s_cols = lane_base + 128 * half, o_cols = lane_base + 256 + 128 * half;
+    const uint32_t q_addr = smem_u32(smem + L::kQ + half * L::kTile);
+    uint32_t n_tiles = 0;                             // tiles of this half so far: phase of s_full
+    uint32_t n_seg = 0, tile = 0;                     // segments of this half; tiles of the CTA (ring index)
+    Walk w = walk_start<RT, KT>(p, share);
+    bool more = w.count > 0;
+    while (more) {
+      const int rows = w.req.n * p.rep.d;
+      const int row = w.rt * RT + half * 128 + lrow;
+      if (w.rt * RT + half * 128 >= rows) {           // nothing in this half
+        tile += w.here;
+        more = walk_next<RT, KT>(p, w);
+        continue;
+      }
+      const bool live = row < rows;
+      const int tok = min(row, rows - 1) / p.rep;
+      const int hq = w.h * p.rep.d + (min(row, rows - 1) - tok * p.rep.d);
+      const int pos = w.req.kv - w.req.n + tok;
+      const int hi = p.causal ? min(w.req.kv, pos + 1) : w.req.kv;
+      const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+      float f;
+      {  // queries: bf16 -> fp16 / 2^e, into this row of the swizzled tile
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (w.req.row0 + tok) * p.q_stride + hq * D);
+        uint4 v[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) amax = fmax3(amax, fabsf(bf16_lo(u[j])), fabsf(bf16_hi(u[j])));
+        }
+        const int e = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 127 - 12, -120), 120);
+        const float inv = p.scale < 0.f ? -pow2(-e) : pow2(-e);       // a negative scale turns the queries round
+        f = fmaxf(fabsf(p.scale) * 1.4426950408889634f * pow2(e), 1.17549435e-38f);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          sts128(q_addr + tile_chunk(lrow, i), pack_f16x2(bf16_lo(v[i].x) * inv, bf16_hi(v[i].x) * inv),
+                 pack_f16x2(bf16_lo(v[i].y) * inv, bf16_hi(v[i].y) * inv), pack_f16x2(bf16_lo(v[i].z) * inv, bf16_hi(v[i].z) * inv),
+                 pack_f16x2(bf16_lo(v[i].w) * inv, bf16_hi(v[i].w) * inv));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[half]);
+      }
+      float m = -INFINITY, l = 0.f;
+      int ev = 0;
+      bool ok = true;
+      for (int j = 0; j < w.here; ++j, ++tile, ++n_tiles) {
+        ok = wait(&s_full[half], n_tiles & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_cols + 32 * c, sr[c]);
+        auto S = [&](int c) { return __uint_as_float(sr[c / 32][c % 32]); };
+        const uint32_t* mk = masks + 4 * (tile % kRowsRing);
+        const uint4 mask = *reinterpret_cast<const uint4*>(mk);
+        float ft = f;
+        float grow = 1.f;                             // change of the values' power of two
+        if constexpr (FMT == kFmtInt4) {
+          ft = fmaxf(f * pow2(kexp[tile % kRowsRing]), 1.17549435e-38f);
+          const int e2 = vexp[tile % kRowsRing];
+          if (j > 0) grow = pow2(max(ev - e2, -126));
+          ev = e2;
+        }
+        tmem_wait_ld();
+        const int base = w.first + j * KT;
+        const bool cut = base < lo || base + KT > hi;
+        if (__any_sync(0xffffffffu, cut || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu)) {
+          const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!((mw[c / 32] >> (c % 32)) & 1) || base + c >= hi || base + c < lo) sr[c / 32][c % 32] = 0xff800000u;
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top[c] = fmaxf(S(c), S(c + 4));
+#pragma unroll
+        for (int c = 8; c < 128; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = fmax3(top[i], S(c + i), S(c + i + 4));
+        const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * ft;
+        const bool move = x > m + kRowsLazy;          // also from -inf
+        float shrink = grow;
+        if (move) {
+          const float c = ex2(m - x);
+          l *= c;
+          shrink *= c;
+          m = x;
+        }
+        if (__any_sync(0xffffffffu, shrink != 1.f) && j > 0) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_cols + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+            tmem_st32(o_cols + c, o);
+          }
+        }
+        const float sub = m == -INFINITY ? 0.f : kRowsShift - m;
+        const float2 f2 = make_float2(ft, ft), b2 = make_float2(sub, sub);
+        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          float2 y = ffma2(make_float2(S(2 * c), S(2 * c + 1)), f2, b2);
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum2[c & 1] = fadd2(sum2[c & 1], y);
+          pk[c] = pack_f16x2(y.x, y.y);
+        }
+        const float2 sum = fadd2(sum2[0], sum2[1]);
+        l += sum.x + sum.y;
+        tmem_st32(s_cols, pk);
+        tmem_st32(s_cols + 32, pk + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[half]);
+      }
+      if (!ok || !wait(&o_full[half], n_seg & 1)) break;
+      ++n_seg;
+      tc_fence_after();
+      const bool split = w.unit > 0 || w.here < w.units;
+      float unscale = 1.f;
+      if constexpr (FMT == kFmtInt4) unscale = pow2(ev);
+      const long long orow = (w.req.row0 + tok) * p.out_stride + hq * D;
+      float* slot = p.partials + (2ll * blockIdx.x + (w.at == share.begin ? 0 : 1)) * SLOT;
+      const float inv = l > 0.f ? unscale / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_cols + c, o);
+        tmem_wait_ld();
+        if (live && !split) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pk[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+            dst[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else if (live) {
+          float4* dst = reinterpret_cast<float4*>(slot + (half * 128 + lrow) * D + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            __stcg(dst + i, make_float4(__uint_as_float(o[4 * i]) * unscale, __uint_as_float(o[4 * i + 1]) * unscale,
+                                        __uint_as_float(o[4 * i + 2]) * unscale, __uint_as_float(o[4 * i + 3]) * unscale));
+        }
+        __syncwarp();
+      }
+      tc_fence_before();                              // O is read before the next segment's MMAs
+      float* lse = p.lse == nullptr ? nullptr : p.lse + static_cast<long long>(w.req.row0 + tok) * p.q_heads + hq;
+      if (!split) {
+        if (live && lse != nullptr) *lse = l > 0.f ? (m - kRowsShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      } else {
+        if (live) __stcg(reinterpret_cast<float2*>(slot + RT * D + 2 * (half * 128 + lrow)), make_float2(m, l));
+        // each half of an item is joined by itself: its four warps arrive together
+        const long long item = w.at - w.unit;
+        const int c0 = share_of(share.base, share.rem, item), c1 = share_of(share.base, share.rem, item + w.units - 1);
+        __threadfence();
+        if (!meet(&join[half], 0)) break;
+        if ((warp & 3) == 0 && lane == 0) {
+          last_flag[half] = arrive_last(&p.counters[2 * c0 + half], p.nonce, c1 - c0 + 1);
+          __threadfence();
+        }
+        if (!meet(&join[half], 1)) break;
+        if (last_flag[half] && live) {
+          const float* part0 = p.partials + (share_begin(share.base, share.rem, c0) == item ? 2ll * c0 : 2ll * c0 + 1) * SLOT;
+          float top = -INFINITY, total = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const float2 ms = __ldcg(reinterpret_cast<const float2*>((c == c0 ? part0 : p.partials + 2ll * c * SLOT) + RT * D + 2 * (half * 128 + lrow)));
+            const float m2 = fmaxf(top, ms.x);
+            if (m2 > -INFINITY) total = total * ex2(top - m2) + ms.y * ex2(ms.x - m2);
+            top = m2;
+          }
+          const float join = total > 0.f ? 1.f / total : 0.f;
+          for (int d = 0; d < D; d += 32) {
+            float acc[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+            for (int c = c0; c <= c1; ++c) {
+              const float* sl = c == c0 ? part0 : p.partials + 2ll * c * SLOT;
+              const float mc = __ldcg(sl + RT * D + 2 * (half * 128 + lrow));
+              const float fc = mc > -INFINITY ? ex2(mc - top) : 0.f;
+              const float4* src = reinterpret_cast<const float4*>(sl + (half * 128 + lrow) * D + d);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 v = __ldcg(src + i);
+                acc[4 * i] = fmaf(v.x, fc, acc[4 * i]), acc[4 * i + 1] = fmaf(v.y, fc, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(v.z, fc, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(v.w, fc, acc[4 * i + 3]);
+              }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(acc[8 * i] * join, acc[8 * i + 1] * join), pack_bf16x2(acc[8 * i + 2] * join, acc[8 * i + 3] * join),
+                                  pack_bf16x2(acc[8 * i + 4] * join, acc[8 * i + 5] * join), pack_bf16x2(acc[8 * i + 6] * join, acc[8 * i + 7] * join));
+          }
+          if (lse != nullptr) *lse = total > 0.f ? (top - kRowsShift + log2f(total)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      more = walk_next<RT, KT>(p, w);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------- codes -> fp16 tiles
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    const int key = threadIdx.x - 256;                // key of a tile
+    constexpr int CW = D / 32;                        // 16-byte words of codes of a key
+    uint32_t tile = 0;
+    int run_ev = -1000;                               // largest value exponent of the segment so far
+    Walk w = walk_start<RT, KT>(p, share);
+    bool more = w.count > 0, ok = true;
+    // pages one tile ahead of the codes, codes one tile ahead of their use
+    struct Raw {
+      uint4 k[CW], v[CW];
+      uint2 ks, vs;
+      bool good;
+    };
+    auto fetch = [&](const Walk& w, int j) {
+      Raw r;
+      const int t = w.first + j * KT + key;
+      const int end = w.k1;
+      r.good = false;
+      r.ks = r.vs = make_uint2(0u, 0u);
+#pragma unroll
+      for (int i = 0; i < CW; ++i) r.k[i] = r.v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < end) {
+        const int page = __ldg(p.table + w.b * p.table_stride + (t >> p.g.page_log2));
+        if (page < 0 || page >= p.g.num_pages) {
+          raise_error(kErrIndex);
+        } else {
+          r.good = true;
+          const int off = t & (p.g.page - 1);
+          const uint8_t* blk = p.g.pool + kv_block(p.g, page, w.h);
+          const uint4* kc = reinterpret_cast<const uint4*>(blk + off * (D / 2));
+          const uint4* vc = reinterpret_cast<const uint4*>(blk + p.g.vc + off * (D / 2));
+#pragma unroll
+          for (int i = 0; i < CW; ++i) r.k[i] = kc[i];
+#pragma unroll
+          for (int i = 0; i < CW; ++i) r.v[i] = vc[i];
+          const uint8_t* ks = blk + p.g.ks + off * SB;
+          const uint8_t* vs = blk + p.g.vs + off * SB;
+          if constexpr (SB == 8) {
+            r.ks = *reinterpret_cast<const uint2*>(ks);
+            r.vs = *reinterpret_cast<const uint2*>(vs);
+          } else if constexpr (SB == 4) {
+            r.ks.x = *reinterpret_cast<const uint32_t*>(ks);
+            r.vs.x = *reinterpret_cast<const uint32_t*>(vs);
+          } else {
+            r.ks.x = *reinterpret_cast<const uint16_t*>(ks);
+            r.vs.x = *reinterpret_cast<const uint16_t*>(vs);
+          }
+        }
+      }
+      return r;
+    };
+    // FP4: scale pair of the 8 codes of chunk c
+    auto fp4_tile = [&](uint32_t addr, const uint4 (&codes)[CW], const uint2& sc) {
+      constexpr int NS = SB;                          // scales of the key
+      uint32_t s2[NS];
+#pragma unroll
+      for (int i = 0; i < NS; i += 2) {
+        const uint32_t word = i < 4 ? sc.x : sc.y;
+        const uint32_t two = e4m3x2_to_f16((word >> (8 * (i & 3))) & 0xffffu);
+        s2[i] = __byte_perm(two, two, 0x1010);
+        if (i + 1 < NS) s2[i + 1] = __byte_perm(two, two, 0x3232);
+      }
+#pragma unroll
+      for (int i = 0; i < CW; ++i) {
+        const uint32_t u[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 4 * i + k;
+          const uint32_t s = s2[c * 8 / kv_group(FMT)];
+          uint32_t h[4];
+          e2m1x8_to_f16(u[k], h);
+          sts128(addr + tile_chunk(key, c), hmul2_u(h[0], s), hmul2_u(h[1], s), hmul2_u(h[2], s), hmul2_u(h[3], s));
+        }
+      }
+    };
+    // INT4: code * scale / 2^e, rounded to fp16, and what the rounding left (LO)
+    auto int4_tile = [&](uint32_t addr, uint32_t addr_lo, const uint4 (&codes)[CW], const uint2& sc, float down, bool lo) {
+#pragma unroll
+      for (int i = 0; i < CW; ++i) {
+        const uint32_t u[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 4 * i + k;
+          const uint16_t bits = static_cast<uint16_t>(c < 8 ? sc.x & 0xffffu : sc.x >> 16);
+          const float s = __half2float(__ushort_as_half(bits)) * down;
+          uint32_t hi[4], rest[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float a = static_cast<float>(static_cast<int>(u[k] << (28 - 8 * x)) >> 28) * s;
+            const float b = static_cast<float>(static_cast<int>(u[k] << (24 - 8 * x)) >> 28) * s;
+            hi[x] = pack_f16x2(a, b);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[x]));
+            rest[x] = pack_f16x2(a - back.x, b - back.y);
+          }
+          sts128(addr + tile_chunk(key, c), hi[0], hi[1], hi[2], hi[3]);
+          if (lo) sts128(addr_lo + tile_chunk(key, c), rest[0], rest[1], rest[2], rest[3]);
+        }
+      }
+    };
+    // exponent of the largest of a key's scales (fp16, at least 2^-24), over the warp
+    auto warp_exponent = [&](uint32_t two) {
+      int e = -24;
+#pragma unroll
+      for (int i = 0; i < SB / 2; ++i) {
+        const float s = fabsf(__half2float(__ushort_as_half(static_cast<uint16_t>(i ? two >> 16 : two & 0xffffu))));
+        e = max(e, static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127);
+      }
+      return __reduce_max_sync(0xffffffffu, min(e, 16));
+    };
+
+    Raw raw;
+    if (more) raw = fetch(w, 0);
+    while (more && ok) {
+      run_ev = -1000;
+      const int here = w.here;
+      for (int j = 0; j < here; ++j, ++tile) {
+        const Raw now = raw;
+        bool end = false;
+        if (j + 1 < here) {
+          raw = fetch(w, j + 1);
+        } else {                                      // the next segment's first tile
+          more = walk_next<RT, KT>(p, w);
+          end = true;
+          if (more) raw = fetch(w, 0);
+        }
+        const unsigned good = __ballot_sync(0xffffffffu, now.good);
+        const uint32_t ks = tile % L::kKStages, vs = tile % L::kVStages;
+        const uint32_t kaddr = smem_u32(smem + L::kK + ks * L::kParts * L::kTile), vaddr = smem_u32(smem + L::kV + vs * L::kTile);
+        int ek = 0;
+        if constexpr (FMT == kFmtInt4) {
+          int* sc = scratch + 8 * (tile & 1);         // written again two tiles on, behind the next tile's barrier
+          const int wk = warp_exponent(now.good ? now.ks.x : 0u), wv = warp_exponent(now.good ? now.vs.x : 0u);
+          if (lane == 0) {
+            sc[warp - 8] = wk;
+            sc[warp - 4] = wv;
+          }
+          if (!meet(exps, tile & 1)) {
+            ok = false;
+            break;
+          }
+          ek = max(max(sc[0], sc[1]), max(sc[2], sc[3]));
+          run_ev = max(run_ev, max(max(sc[4], sc[5]), max(sc[6], sc[7])));
+        }
+        if (!wait(&k_empty[ks], ((tile / L::kKStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) masks[4 * (tile % kRowsRing) + warp - 8] = good;
+        if constexpr (FMT == kFmtInt4) {
+          if (threadIdx.x == 256) {
+            kexp[tile % kRowsRing] = ek;
+            vexp[tile % kRowsRing] = run_ev;
+          }
+          int4_tile(kaddr, kaddr + L::kTile, now.k, now.ks, pow2(-ek), true);
+        } else {
+          fp4_tile(kaddr, now.k, now.ks);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[ks]);
+        if (!wait(&v_empty[vs], ((tile / L::kVStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if constexpr (FMT == kFmtInt4)
+          int4_tile(vaddr, 0u, now.v, now.vs, pow2(-run_ev), false);
+        else
+          fp4_tile(vaddr, now.v, now.vs);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[vs]);
+        if (end) {
+          ++tile;
+          break;
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 12) {
+      // ---------------------------------------------------------------- MMA
+      constexpr uint32_t id_s = idesc_f16_f32(128, KT, false), id_o = idesc_f16_f32(128, D, true);
+      uint32_t tile = 0, pf[2] = {0, 0}, qf[2] = {0, 0};
+      Walk w = walk_start<RT, KT>(p, share);
+      bool more = w.count > 0;
+      const uint32_t q0 = smem_u32(smem + L::kQ);
+      auto scores = [&](int half, uint32_t stage) {
+        if (elect_one()) {
+          const uint32_t qa = q0 + half * L::kTile, ka = smem_u32(smem + L::kK + stage * L::kParts * L::kTile);
+#pragma unroll
+          for (int part = 0; part < L::kParts; ++part)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k / 4) * L::kPanel + (k % 4) * 32;
+              mma_f16_ss(tmem + 128 * half, make_kmajor_desc(qa + off, 128), make_kmajor_desc(ka + part * L::kTile + off, 128), id_s,
+                         part > 0 || k > 0);
+            }
+          tc_commit(&s_full[half]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int half, uint32_t stage, bool first) {
+        if (elect_one()) {
+          const uint32_t va = smem_u32(smem + L::kV + stage * L::kTile);
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * k,
+                       make_sdesc(va + k * 2048, L::kPanel, 1024, kSwizzle128B), id_o, !first || k > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      while (more) {
+        const int halves = w.rt * RT + 128 < w.req.n * p.rep.d ? 2 : 1;
+        bool ok = true;
+        for (int i = 0; i < halves && ok; ++i) ok = wait(&q_full[i], qf[i]++ & 1);
+        ok = ok && wait(&k_full[tile % L::kKStages], (tile / L::kKStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < halves; ++i) scores(i, tile % L::kKStages);
+        commit(&k_empty[tile % L::kKStages]);
+        for (int j = 0; j < w.here && ok; ++j, ++tile) {
+          const bool next = j + 1 < w.here;
+          const uint32_t ks = (tile + 1) % L::kKStages, vs = tile % L::kVStages;
+          for (int i = 0; i < halves && ok; ++i) {
+            ok = wait(&p_full[i], pf[i]++ & 1);
+            if (ok && i == 0) ok = wait(&v_full[vs], (tile / L::kVStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(i, vs, j == 0);
+            if (next) {
+              if (i == 0) {
+                ok = wait(&k_full[ks], ((tile + 1) / L::kKStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              scores(i, ks);
+            } else {
+              commit(&o_full[i]);
+            }
+          }
+          if (!ok) break;
+          commit(&v_empty[vs]);
+          if (next) commit(&k_empty[ks]);
+        }
+        if (!ok) break;
+        more = walk_next<RT, KT>(p, w);
+      }
+      // everything issued has retired before TMEM is released
+      commit(mma_done);
+      if (!warp_wait(mma_done, 0, drain_budget(budget), nullptr) && lane == 0) raise_error(kErrWaitAttn);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace svdq
