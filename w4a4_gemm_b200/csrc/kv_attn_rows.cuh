@@ -4,7 +4,7 @@
 // A tile is 256 rows (a row is a token and one query head of the key head's
 // group) as two halves of 128, walked over the keys 128 at a time:
 //   S_w = Q_w K^T   (128 x 128 x D, operands in shared memory, TMEM columns 128 w)
-//   P_w = exp2(S_w f - m), fp16, written over S_w in TMEM
+//   P_w = exp2(S_w f - m), fp16, written over the second half of S_w in TMEM
 //   O_w += P_w V    (128 x D x 128, P from TMEM, V from shared memory, columns 256 + 128 w)
 // Sixteen warps: two groups of four keep the softmax of a half each (a thread per
 // row: maximum, sum and row factor are private to it), four turn codes into fp16
@@ -65,6 +65,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -295,12 +303,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         ok = wait(&s_full[half], n_tiles & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_cols + 32 * c, sr[c]);
-        auto S = [&](int c) { return __uint_as_float(sr[c / 32][c % 32]); };
-        const uint32_t* mk = masks + 4 * (tile % kRowsRing);
-        const uint4 mask = *reinterpret_cast<const uint4*>(mk);
+        const uint4 mask = *reinterpret_cast<const uint4*>(masks + 4 * (tile % kRowsRing));
         float ft = f;
         float grow = 1.f;                             // change of the values' power of two
         if constexpr (FMT == kFmtInt4) {
@@ -309,22 +312,34 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           if (j > 0) grow = pow2(max(ev - e2, -126));
           ev = e2;
         }
-        tmem_wait_ld();
         const int base = w.first + j * KT;
         const bool cut = base < lo || base + KT > hi;
-        if (__any_sync(0xffffffffu, cut || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu)) {
-          const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
+        const bool masked = __any_sync(0xffffffffu, cut || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu);
+        // The row is read twice, 32 columns at a time: for its maximum upwards, for its weights downwards, so
+        // that the weights of columns 32c .. land in columns 64 + 16c .. behind what is still to be read.
+        uint32_t sr[2][32];
+        auto hide = [&](uint32_t (&x)[32], int c) {   // columns that this row does not see
+          uint32_t see = c == 0 ? mask.x : c == 1 ? mask.y : c == 2 ? mask.z : mask.w;
+          const int b0 = base + 32 * c, under = lo - b0, over = hi - b0;
+          if (under > 0) see &= under >= 32 ? 0u : 0xffffffffu << under;
+          if (over < 32) see &= over <= 0 ? 0u : 0xffffffffu >> (32 - over);
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!((mw[c / 32] >> (c % 32)) & 1) || base + c >= hi || base + c < lo) sr[c / 32][c % 32] = 0xff800000u;
+          for (int i = 0; i < 32; ++i)
+            if (!((see >> i) & 1)) x[i] = 0xff800000u;
+        };
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld32(s_cols, sr[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld();
+          if (c < 3) tmem_ld32(s_cols + 32 * (c + 1), sr[(c + 1) & 1]);
+          uint32_t(&x)[32] = sr[c & 1];
+          if (masked) hide(x, c);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[k] = fmax3(top[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + k + 4]));
         }
-        float top[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = fmaxf(S(c), S(c + 4));
-#pragma unroll
-        for (int c = 8; c < 128; c += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top[i] = fmax3(top[i], S(c + i), S(c + i + 4));
         const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * ft;
         const bool move = x > m + kRowsLazy;          // also from -inf
         float shrink = grow;
@@ -334,33 +349,39 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           shrink *= c;
           m = x;
         }
-        if (__any_sync(0xffffffffu, shrink != 1.f) && j > 0) {
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_cols + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-            tmem_st32(o_cols + c, o);
-          }
-        }
+        tmem_ld32(s_cols + 64, sr[0]);                // columns 64 .. 95: the next to be used (96 .. are in sr[1])
         const float sub = m == -INFINITY ? 0.f : kRowsShift - m;
         const float2 f2 = make_float2(ft, ft), b2 = make_float2(sub, sub);
         float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t pk[64];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          float2 y = ffma2(make_float2(S(2 * c), S(2 * c + 1)), f2, b2);
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          sum2[c & 1] = fadd2(sum2[c & 1], y);
-          pk[c] = pack_f16x2(y.x, y.y);
+        for (int c = 3; c >= 0; --c) {
+          uint32_t(&y)[32] = sr[c & 1];
+          if (masked && c < 3) hide(y, c);
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 v = ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), f2, b2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum2[i & 1] = fadd2(sum2[i & 1], v);
+            pk[i] = pack_f16x2(v.x, v.y);
+          }
+          if (c > 0) tmem_wait_ld();                  // columns of step c - 1 are here
+          tmem_st16(s_cols + 64 + 16 * c, pk);
+          if (c > 1) tmem_ld32(s_cols + 32 * (c - 2), sr[c & 1]);
         }
         const float2 sum = fadd2(sum2[0], sum2[1]);
         l += sum.x + sum.y;
-        tmem_st32(s_cols, pk);
-        tmem_st32(s_cols + 32, pk + 32);
+        if (__any_sync(0xffffffffu, shrink != 1.f) && j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            tmem_ld32(o_cols + c, sr[0]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sr[0][i] = __float_as_uint(__uint_as_float(sr[0][i]) * shrink);
+            tmem_st32(o_cols + c, sr[0]);
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -660,7 +681,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           const uint32_t va = smem_u32(smem + L::kV + stage * L::kTile);
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * k,
+            mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 64 + 8 * k,
                        make_sdesc(va + k * 2048, L::kPanel, 1024, kSwizzle128B), id_o, !first || k > 0);
         }
         __syncwarp();
