@@ -92,7 +92,7 @@ int kv_device(int* dev) {
       cudaFuncAttributes at;
       SVDQ_CUDA(cudaFuncGetAttributes(&at, k));
       // its warp groups raise their registers to 184 out of what the block starts with: all of 65536, or they would wait
-      if (at.numRegs * kRowsThreads < 2 * 128 * 184 + 128 * 104 + 128 * 40) return SVDQ_ERR_CUDA;
+      if (at.numRegs * kRowsThreads < 2 * 128 * 184 + 128 * 80 + 128 * 64) return SVDQ_ERR_CUDA;
     }
   g_kv_set[*dev].store(true, std::memory_order_release);
   return SVDQ_OK;

@@ -4,7 +4,7 @@
 // A tile is 256 rows (a row is a token and one query head of the key head's
 // group) as two halves of 128, walked over the keys 128 at a time:
 //   S_w = Q_w K^T   (128 x 128 x D, operands in shared memory, TMEM columns 128 w)
-//   P_w = exp2(S_w f - m), fp16, written over the second half of S_w in TMEM
+//   P_w = exp2(S_w f - m), fp16, written over the first half of S_w in TMEM
 //   O_w += P_w V    (128 x D x 128, P from TMEM, V from shared memory, columns 256 + 128 w)
 // Sixteen warps: two groups of four keep the softmax of a half each (a thread per
 // row: maximum, sum and row factor are private to it), four turn codes into fp16
@@ -271,31 +271,42 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       const int pos = w.req.kv - w.req.n + tok;
       const int hi = p.causal ? min(w.req.kv, pos + 1) : w.req.kv;
       const int lo = p.window > 0 ? pos - p.window + 1 : 0;
-      float f;
-      {  // queries: bf16 -> fp16 / 2^e, into this row of the swizzled tile
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (w.req.row0 + tok) * p.q_stride + hq * D);
-        uint4 v[D / 8];
+      // Queries: bf16 -> fp16 / 2^e, into the swizzled tile.  The warp loads its 32 rows D / 8 lanes a row, so a
+      // load covers whole lines; a row's exponent goes to the lane that keeps the row.
+      int e_row = 0;
+      {
+        constexpr int LPR = D / 8, RPL = 32 / LPR;    // lanes of a row, rows of a load
+        const int c = lane % LPR;
+        uint4 v[32 / RPL];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        float amax = 0.f;
+        for (int i = 0; i < 32 / RPL; ++i) {
+          const int gr = w.rt * RT + half * 128 + (warp & 3) * 32 + i * RPL + lane / LPR;
+          const int tk = min(gr, rows - 1) / p.rep;
+          const __nv_bfloat16* src = p.q + (w.req.row0 + tk) * p.q_stride + (w.h * p.rep.d + (min(gr, rows - 1) - tk * p.rep.d)) * D;
+          v[i] = gr < rows ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < 32 / RPL; ++i) {
           const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          float amax = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) amax = fmax3(amax, fabsf(bf16_lo(u[j])), fabsf(bf16_hi(u[j])));
-        }
-        const int e = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 127 - 12, -120), 120);
-        const float inv = p.scale < 0.f ? -pow2(-e) : pow2(-e);       // a negative scale turns the queries round
-        f = fmaxf(fabsf(p.scale) * 1.4426950408889634f * pow2(e), 1.17549435e-38f);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          sts128(q_addr + tile_chunk(lrow, i), pack_f16x2(bf16_lo(v[i].x) * inv, bf16_hi(v[i].x) * inv),
-                 pack_f16x2(bf16_lo(v[i].y) * inv, bf16_hi(v[i].y) * inv), pack_f16x2(bf16_lo(v[i].z) * inv, bf16_hi(v[i].z) * inv),
-                 pack_f16x2(bf16_lo(v[i].w) * inv, bf16_hi(v[i].w) * inv));
+          for (int x = 1; x < LPR; x *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
+          const int e = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 127 - 12, -120), 120);
+          const float inv = p.scale < 0.f ? -pow2(-e) : pow2(-e);     // a negative scale turns the queries round
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = pack_f16x2(bf16_lo(u[j]) * inv, bf16_hi(u[j]) * inv);
+          sts128(q_addr + tile_chunk((warp & 3) * 32 + i * RPL + lane / LPR, c), h[0], h[1], h[2], h[3]);
+          const int from = __shfl_sync(0xffffffffu, e, (lane % RPL) * LPR);
+          if (lane / RPL == i) e_row = from;
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[half]);
       }
+      const float f = fmaxf(fabsf(p.scale) * 1.4426950408889634f * pow2(e_row), 1.17549435e-38f);
       float m = -INFINITY, l = 0.f;
       int ev = 0;
       bool ok = true;
@@ -315,31 +326,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         const int base = w.first + j * KT;
         const bool cut = base < lo || base + KT > hi;
         const bool masked = __any_sync(0xffffffffu, cut || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu);
-        // The row is read twice, 32 columns at a time: for its maximum upwards, for its weights downwards, so
-        // that the weights of columns 32c .. land in columns 64 + 16c .. behind what is still to be read.
-        uint32_t sr[2][32];
-        auto hide = [&](uint32_t (&x)[32], int c) {   // columns that this row does not see
-          uint32_t see = c == 0 ? mask.x : c == 1 ? mask.y : c == 2 ? mask.z : mask.w;
-          const int b0 = base + 32 * c, under = lo - b0, over = hi - b0;
-          if (under > 0) see &= under >= 32 ? 0u : 0xffffffffu << under;
-          if (over < 32) see &= over <= 0 ? 0u : 0xffffffffu >> (32 - over);
+        uint32_t sr[4][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((see >> i) & 1)) x[i] = 0xff800000u;
-        };
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_cols + 32 * c, sr[c]);
+        tmem_wait_ld();
+        if (masked) {
+          const uint32_t mw[4] = {mask.x, mask.y, mask.z, mask.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t see = mw[c];                     // columns that this row sees
+            const int b0 = base + 32 * c, under = lo - b0, over = hi - b0;
+            if (under > 0) see &= under >= 32 ? 0u : 0xffffffffu << under;
+            if (over < 32) see &= over <= 0 ? 0u : 0xffffffffu >> (32 - over);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1)) sr[c][i] = 0xff800000u;
+          }
+        }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld32(s_cols, sr[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld();
-          if (c < 3) tmem_ld32(s_cols + 32 * (c + 1), sr[(c + 1) & 1]);
-          uint32_t(&x)[32] = sr[c & 1];
-          if (masked) hide(x, c);
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top[k] = fmax3(top[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + k + 4]));
-        }
+            for (int k = 0; k < 4; ++k) top[k] = fmax3(top[k], __uint_as_float(sr[c][i + k]), __uint_as_float(sr[c][i + k + 4]));
         const float x = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * ft;
         const bool move = x > m + kRowsLazy;          // also from -inf
         float shrink = grow;
@@ -349,37 +359,33 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           shrink *= c;
           m = x;
         }
-        tmem_ld32(s_cols + 64, sr[0]);                // columns 64 .. 95: the next to be used (96 .. are in sr[1])
         const float sub = m == -INFINITY ? 0.f : kRowsShift - m;
         const float2 f2 = make_float2(ft, ft), b2 = make_float2(sub, sub);
         float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 3; c >= 0; --c) {
-          uint32_t(&y)[32] = sr[c & 1];
-          if (masked && c < 3) hide(y, c);
+        for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float2 v = ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), f2, b2);
+            float2 v = ffma2(make_float2(__uint_as_float(sr[c][2 * i]), __uint_as_float(sr[c][2 * i + 1])), f2, b2);
             v.x = ex2(v.x);
             v.y = ex2(v.y);
             sum2[i & 1] = fadd2(sum2[i & 1], v);
             pk[i] = pack_f16x2(v.x, v.y);
           }
-          if (c > 0) tmem_wait_ld();                  // columns of step c - 1 are here
-          tmem_st16(s_cols + 64 + 16 * c, pk);
-          if (c > 1) tmem_ld32(s_cols + 32 * (c - 2), sr[c & 1]);
+          tmem_st16(s_cols + 16 * c, pk);
         }
         const float2 sum = fadd2(sum2[0], sum2[1]);
         l += sum.x + sum.y;
         if (__any_sync(0xffffffffu, shrink != 1.f) && j > 0) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
-            tmem_ld32(o_cols + c, sr[0]);
+            uint32_t o[32];
+            tmem_ld32(o_cols + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sr[0][i] = __float_as_uint(__uint_as_float(sr[0][i]) * shrink);
-            tmem_st32(o_cols + c, sr[0]);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+            tmem_st32(o_cols + c, o);
           }
         }
         tmem_wait_st();
@@ -393,40 +399,63 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       const bool split = w.unit > 0 || w.here < w.units;
       float unscale = 1.f;
       if constexpr (FMT == kFmtInt4) unscale = pow2(ev);
-      const long long orow = (w.req.row0 + tok) * p.out_stride + hq * D;
-      float* slot = p.partials + (2ll * blockIdx.x + (w.at == share.begin ? 0 : 1)) * SLOT;
+      // The finished rows leave through the half's query tile (its MMAs are done): a lane writes its row as
+      // 16-byte chunks, swizzled, and the warp copies its 32 rows out D / 8 lanes a row.
+      const uint32_t stage = q_addr + (warp & 3) * 32 * (D * 2);
+      auto put = [&](int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        sts128(stage + lane * (D * 2) + ((chunk ^ (lane & 7)) << 4), a, b, c, d);
+      };
+      auto copy_out = [&]() {
+        __syncwarp();
+        constexpr int LPR = D / 8, RPL = 32 / LPR;
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPL; ++i) {
+          const int lr = i * RPL + lane / LPR, c = lane % LPR;
+          const int gr = w.rt * RT + half * 128 + (warp & 3) * 32 + lr;
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage + lr * (D * 2) + ((c ^ (lr & 7)) << 4)) : "memory");
+          if (gr < rows) {
+            const int tk = gr / p.rep;
+            *reinterpret_cast<uint4*>(p.out + (w.req.row0 + tk) * p.out_stride + (w.h * p.rep.d + (gr - tk * p.rep.d)) * D + 8 * c) = v;
+          }
+        }
+        __syncwarp();
+      };
+      // a partial result: [D / 4][256] float4, so that the lanes of a store are neighbours; then [256] (max, sum)
+      float4* slot = reinterpret_cast<float4*>(p.partials + (2ll * blockIdx.x + (w.at == share.begin ? 0 : 1)) * SLOT);
+      const int srow = half * 128 + lrow;
       const float inv = l > 0.f ? unscale / l : 0.f;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tmem_ld32(o_cols + c, o);
         tmem_wait_ld();
-        if (live && !split) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + orow + c);
+        if (!split) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t pk[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               pk[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-            dst[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            put(c / 8 + i, pk[0], pk[1], pk[2], pk[3]);
           }
-        } else if (live) {
-          float4* dst = reinterpret_cast<float4*>(slot + (half * 128 + lrow) * D + c);
+        } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            __stcg(dst + i, make_float4(__uint_as_float(o[4 * i]) * unscale, __uint_as_float(o[4 * i + 1]) * unscale,
-                                        __uint_as_float(o[4 * i + 2]) * unscale, __uint_as_float(o[4 * i + 3]) * unscale));
+            __stcg(slot + (c / 4 + i) * RT + srow,
+                   make_float4(__uint_as_float(o[4 * i]) * unscale, __uint_as_float(o[4 * i + 1]) * unscale,
+                               __uint_as_float(o[4 * i + 2]) * unscale, __uint_as_float(o[4 * i + 3]) * unscale));
         }
-        __syncwarp();
       }
       tc_fence_before();                              // O is read before the next segment's MMAs
-      float* lse = p.lse == nullptr ? nullptr : p.lse + static_cast<long long>(w.req.row0 + tok) * p.q_heads + hq;
+      float* lse = p.lse == nullptr || !live ? nullptr : p.lse + static_cast<long long>(w.req.row0 + tok) * p.q_heads + hq;
       if (!split) {
-        if (live && lse != nullptr) *lse = l > 0.f ? (m - kRowsShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        copy_out();
+        if (lse != nullptr) *lse = l > 0.f ? (m - kRowsShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {
-        if (live) __stcg(reinterpret_cast<float2*>(slot + RT * D + 2 * (half * 128 + lrow)), make_float2(m, l));
-        // each half of an item is joined by itself: its four warps arrive together
+        __stcg(reinterpret_cast<float2*>(slot + RT * (D / 4)) + srow, make_float2(m, l));
+        // each half of an item is joined by itself, by the CTA whose four warps arrive last
         const long long item = w.at - w.unit;
         const int c0 = share_of(share.base, share.rem, item), c1 = share_of(share.base, share.rem, item + w.units - 1);
         __threadfence();
@@ -436,38 +465,40 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           __threadfence();
         }
         if (!meet(&join[half], 1)) break;
-        if (last_flag[half] && live) {
+        if (last_flag[half]) {
           const float* part0 = p.partials + (share_begin(share.base, share.rem, c0) == item ? 2ll * c0 : 2ll * c0 + 1) * SLOT;
+          auto part = [&](int c) { return reinterpret_cast<const float4*>(c == c0 ? part0 : p.partials + 2ll * c * SLOT); };
           float top = -INFINITY, total = 0.f;
           for (int c = c0; c <= c1; ++c) {
-            const float2 ms = __ldcg(reinterpret_cast<const float2*>((c == c0 ? part0 : p.partials + 2ll * c * SLOT) + RT * D + 2 * (half * 128 + lrow)));
+            const float2 ms = __ldcg(reinterpret_cast<const float2*>(part(c) + RT * (D / 4)) + srow);
             const float m2 = fmaxf(top, ms.x);
             if (m2 > -INFINITY) total = total * ex2(top - m2) + ms.y * ex2(ms.x - m2);
             top = m2;
           }
-          const float join = total > 0.f ? 1.f / total : 0.f;
-          for (int d = 0; d < D; d += 32) {
-            float acc[32];
+          const float each = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll 1
+          for (int d = 0; d < D / 4; d += 8) {
+            float4 acc[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+            for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int c = c0; c <= c1; ++c) {
-              const float* sl = c == c0 ? part0 : p.partials + 2ll * c * SLOT;
-              const float mc = __ldcg(sl + RT * D + 2 * (half * 128 + lrow));
-              const float fc = mc > -INFINITY ? ex2(mc - top) : 0.f;
-              const float4* src = reinterpret_cast<const float4*>(sl + (half * 128 + lrow) * D + d);
+              const float mc = __ldcg(reinterpret_cast<const float2*>(part(c) + RT * (D / 4)) + srow).x;
+              const float fc = mc > -INFINITY ? ex2(mc - top) * each : 0.f;
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __ldcg(part(c) + (d + i) * RT + srow);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 v = __ldcg(src + i);
-                acc[4 * i] = fmaf(v.x, fc, acc[4 * i]), acc[4 * i + 1] = fmaf(v.y, fc, acc[4 * i + 1]);
-                acc[4 * i + 2] = fmaf(v.z, fc, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(v.w, fc, acc[4 * i + 3]);
+                acc[i].x = fmaf(v[i].x, fc, acc[i].x), acc[i].y = fmaf(v[i].y, fc, acc[i].y);
+                acc[i].z = fmaf(v[i].z, fc, acc[i].z), acc[i].w = fmaf(v[i].w, fc, acc[i].w);
               }
             }
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow + d);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16x2(acc[8 * i] * join, acc[8 * i + 1] * join), pack_bf16x2(acc[8 * i + 2] * join, acc[8 * i + 3] * join),
-                                  pack_bf16x2(acc[8 * i + 4] * join, acc[8 * i + 5] * join), pack_bf16x2(acc[8 * i + 6] * join, acc[8 * i + 7] * join));
+              put(d / 2 + i, pack_bf16x2(acc[2 * i].x, acc[2 * i].y), pack_bf16x2(acc[2 * i].z, acc[2 * i].w),
+                  pack_bf16x2(acc[2 * i + 1].x, acc[2 * i + 1].y), pack_bf16x2(acc[2 * i + 1].z, acc[2 * i + 1].w));
           }
+          copy_out();
           if (lse != nullptr) *lse = total > 0.f ? (top - kRowsShift + log2f(total)) * 0.6931471805599453f : -INFINITY;
         }
       }
@@ -475,53 +506,47 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
     }
   } else if (warp < 12) {
     // ------------------------------------------------------- codes -> fp16 tiles
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const int key = threadIdx.x - 256;                // key of a tile
     constexpr int CW = D / 32;                        // 16-byte words of codes of a key
     uint32_t tile = 0;
     int run_ev = -1000;                               // largest value exponent of the segment so far
     Walk w = walk_start<RT, KT>(p, share);
-    bool more = w.count > 0, ok = true;
-    // pages one tile ahead of the codes, codes one tile ahead of their use
+    bool more = w.count > 0;
+    // A tile's key codes are loaded while the values of the tile before are turned over, and its value codes while
+    // its keys are; its page is looked up a tile ahead.  A key past the segment or in a bad page reads as zeros.
     struct Raw {
-      uint4 k[CW], v[CW];
-      uint2 ks, vs;
-      bool good;
+      uint4 c[CW];
+      uint2 s;
     };
-    auto fetch = [&](const Walk& w, int j) {
-      Raw r;
+    auto page_of = [&](const Walk& w, int j) {
       const int t = w.first + j * KT + key;
-      const int end = w.k1;
-      r.good = false;
-      r.ks = r.vs = make_uint2(0u, 0u);
+      if (t >= w.k1) return -1;
+      const int page = p.table[w.b * p.table_stride + (t >> p.g.page_log2)];
+      if (page < 0 || page >= p.g.num_pages) {
+        raise_error(kErrIndex);
+        return -1;
+      }
+      return page;
+    };
+    auto fetch = [&](int t, int page, int h, bool value) {
+      Raw r;
+      r.s = make_uint2(0u, 0u);
 #pragma unroll
-      for (int i = 0; i < CW; ++i) r.k[i] = r.v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < end) {
-        const int page = __ldg(p.table + w.b * p.table_stride + (t >> p.g.page_log2));
-        if (page < 0 || page >= p.g.num_pages) {
-          raise_error(kErrIndex);
+      for (int i = 0; i < CW; ++i) r.c[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (page >= 0) {
+        const int off = t & (p.g.page - 1);
+        const uint8_t* blk = p.g.pool + kv_block(p.g, page, h) + (value ? p.g.vc : 0);
+        const uint4* c = reinterpret_cast<const uint4*>(blk + off * (D / 2));
+#pragma unroll
+        for (int i = 0; i < CW; ++i) r.c[i] = c[i];
+        const uint8_t* sc = blk + p.g.ks + off * SB;
+        if constexpr (SB == 8) {
+          r.s = *reinterpret_cast<const uint2*>(sc);
+        } else if constexpr (SB == 4) {
+          r.s.x = *reinterpret_cast<const uint32_t*>(sc);
         } else {
-          r.good = true;
-          const int off = t & (p.g.page - 1);
-          const uint8_t* blk = p.g.pool + kv_block(p.g, page, w.h);
-          const uint4* kc = reinterpret_cast<const uint4*>(blk + off * (D / 2));
-          const uint4* vc = reinterpret_cast<const uint4*>(blk + p.g.vc + off * (D / 2));
-#pragma unroll
-          for (int i = 0; i < CW; ++i) r.k[i] = kc[i];
-#pragma unroll
-          for (int i = 0; i < CW; ++i) r.v[i] = vc[i];
-          const uint8_t* ks = blk + p.g.ks + off * SB;
-          const uint8_t* vs = blk + p.g.vs + off * SB;
-          if constexpr (SB == 8) {
-            r.ks = *reinterpret_cast<const uint2*>(ks);
-            r.vs = *reinterpret_cast<const uint2*>(vs);
-          } else if constexpr (SB == 4) {
-            r.ks.x = *reinterpret_cast<const uint32_t*>(ks);
-            r.vs.x = *reinterpret_cast<const uint32_t*>(vs);
-          } else {
-            r.ks.x = *reinterpret_cast<const uint16_t*>(ks);
-            r.vs.x = *reinterpret_cast<const uint16_t*>(vs);
-          }
+          r.s.x = *reinterpret_cast<const uint16_t*>(sc);
         }
       }
       return r;
@@ -585,149 +610,151 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       return __reduce_max_sync(0xffffffffu, min(e, 16));
     };
 
-    Raw raw;
-    if (more) raw = fetch(w, 0);
-    while (more && ok) {
-      run_ev = -1000;
-      const int here = w.here;
-      for (int j = 0; j < here; ++j, ++tile) {
-        const Raw now = raw;
-        bool end = false;
-        if (j + 1 < here) {
-          raw = fetch(w, j + 1);
-        } else {                                      // the next segment's first tile
-          more = walk_next<RT, KT>(p, w);
-          end = true;
-          if (more) raw = fetch(w, 0);
-        }
-        const unsigned good = __ballot_sync(0xffffffffu, now.good);
-        const uint32_t ks = tile % L::kKStages, vs = tile % L::kVStages;
-        const uint32_t kaddr = smem_u32(smem + L::kK + ks * L::kParts * L::kTile), vaddr = smem_u32(smem + L::kV + vs * L::kTile);
-        int ek = 0;
-        if constexpr (FMT == kFmtInt4) {
-          int* sc = scratch + 8 * (tile & 1);         // written again two tiles on, behind the next tile's barrier
-          const int wk = warp_exponent(now.good ? now.ks.x : 0u), wv = warp_exponent(now.good ? now.vs.x : 0u);
-          if (lane == 0) {
-            sc[warp - 8] = wk;
-            sc[warp - 4] = wv;
-          }
-          if (!meet(exps, tile & 1)) {
-            ok = false;
-            break;
-          }
-          ek = max(max(sc[0], sc[1]), max(sc[2], sc[3]));
-          run_ev = max(run_ev, max(max(sc[4], sc[5]), max(sc[6], sc[7])));
-        }
-        if (!wait(&k_empty[ks], ((tile / L::kKStages) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) masks[4 * (tile % kRowsRing) + warp - 8] = good;
-        if constexpr (FMT == kFmtInt4) {
-          if (threadIdx.x == 256) {
-            kexp[tile % kRowsRing] = ek;
-            vexp[tile % kRowsRing] = run_ev;
-          }
-          int4_tile(kaddr, kaddr + L::kTile, now.k, now.ks, pow2(-ek), true);
-        } else {
-          fp4_tile(kaddr, now.k, now.ks);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[ks]);
-        if (!wait(&v_empty[vs], ((tile / L::kVStages) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if constexpr (FMT == kFmtInt4)
-          int4_tile(vaddr, 0u, now.v, now.vs, pow2(-run_ev), false);
-        else
-          fp4_tile(vaddr, now.v, now.vs);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[vs]);
-        if (end) {
-          ++tile;
-          break;
-        }
+    Raw k, v;
+    int page = -1, page_next = -1, at = 0;            // of the tile in k and v, of the one after; the tile's key
+    if (more) {
+      page = page_of(w, 0);
+      at = w.first + key;
+      k = fetch(at, page, w.h, false);
+      v = fetch(at, page, w.h, true);
+    }
+    int j = 0, next_at = 0, next_h = 0;
+    for (; more; ++tile) {
+      // the tile after this one, maybe of the next segment
+      const bool end = j + 1 == w.here, fresh = j == 0;
+      if (end) {
+        more = walk_next<RT, KT>(p, w);
+        j = 0;
+      } else {
+        ++j;
       }
+      if (more) {
+        page_next = page_of(w, j);
+        next_at = w.first + j * KT + key;
+        next_h = w.h;
+      } else {
+        page_next = -1;
+      }
+      const unsigned good = __ballot_sync(0xffffffffu, page >= 0);
+      const uint32_t ks = tile % L::kKStages, vs = tile % L::kVStages;
+      const uint32_t kaddr = smem_u32(smem + L::kK + ks * L::kParts * L::kTile), vaddr = smem_u32(smem + L::kV + vs * L::kTile);
+      int ek = 0;
+      if constexpr (FMT == kFmtInt4) {
+        if (fresh) run_ev = -1000;
+        int* sc = scratch + 8 * (tile & 1);           // written again two tiles on, behind the next tile's barrier
+        const int wk = warp_exponent(k.s.x), wv = warp_exponent(v.s.x);
+        if (lane == 0) {
+          sc[warp - 8] = wk;
+          sc[warp - 4] = wv;
+        }
+        if (!meet(exps, tile & 1)) break;
+        ek = max(max(sc[0], sc[1]), max(sc[2], sc[3]));
+        run_ev = max(run_ev, max(max(sc[4], sc[5]), max(sc[6], sc[7])));
+      }
+      if (!wait(&k_empty[ks], ((tile / L::kKStages) & 1) ^ 1)) break;
+      if (lane == 0) masks[4 * (tile % kRowsRing) + warp - 8] = good;
+      if constexpr (FMT == kFmtInt4) {
+        if (threadIdx.x == 256) {
+          kexp[tile % kRowsRing] = ek;
+          vexp[tile % kRowsRing] = run_ev;
+        }
+        int4_tile(kaddr, kaddr + L::kTile, k.c, k.s, pow2(-ek), true);
+      } else {
+        fp4_tile(kaddr, k.c, k.s);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[ks]);
+      k = fetch(next_at, page_next, next_h, false);
+      if (!wait(&v_empty[vs], ((tile / L::kVStages) & 1) ^ 1)) break;
+      if constexpr (FMT == kFmtInt4)
+        int4_tile(vaddr, 0u, v.c, v.s, pow2(-run_ev), false);
+      else
+        fp4_tile(vaddr, v.c, v.s);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[vs]);
+      v = fetch(next_at, page_next, next_h, true);
+      page = page_next;
+      at = next_at;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12) {
       // ---------------------------------------------------------------- MMA
-      constexpr uint32_t id_s = idesc_f16_f32(128, KT, false), id_o = idesc_f16_f32(128, D, true);
-      uint32_t tile = 0, pf[2] = {0, 0}, qf[2] = {0, 0};
-      Walk w = walk_start<RT, KT>(p, share);
-      bool more = w.count > 0;
-      const uint32_t q0 = smem_u32(smem + L::kQ);
-      auto scores = [&](int half, uint32_t stage) {
-        if (elect_one()) {
-          const uint32_t qa = q0 + half * L::kTile, ka = smem_u32(smem + L::kK + stage * L::kParts * L::kTile);
+      // One lane waits and issues; the others meet it behind the loop.
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_f16_f32(128, KT, false), id_o = idesc_f16_f32(128, D, true);
+        uint32_t tile = 0, pf[2] = {0, 0}, qf[2] = {0, 0};
+        Walk w = walk_start<RT, KT>(p, share);
+        bool more = w.count > 0, ok = true;
+        const uint64_t qd = make_kmajor_desc(smem_u32(smem + L::kQ), 128), kd = make_kmajor_desc(smem_u32(smem + L::kK), 128);
+        const uint64_t vd = make_sdesc(smem_u32(smem + L::kV), L::kPanel, 1024, kSwizzle128B);
+        auto wait1 = [&](uint64_t* bar, uint32_t parity) {
+          if (mbar_wait(bar, parity, budget, const_cast<int*>(abort_flag))) return true;
+          if (!*abort_flag) raise_error(kErrWaitAttn);
+          *abort_flag = 1;
+          return false;
+        };
+        // descriptors count addresses in 16 bytes: offsets are added to the low word's field
+        auto scores = [&](int half, uint32_t stage) {
 #pragma unroll
           for (int part = 0; part < L::kParts; ++part)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = (k / 4) * L::kPanel + (k % 4) * 32;
-              mma_f16_ss(tmem + 128 * half, make_kmajor_desc(qa + off, 128), make_kmajor_desc(ka + part * L::kTile + off, 128), id_s,
+              mma_f16_ss(tmem + 128 * half, qd + ((half * L::kTile + off) >> 4), kd + (((stage * L::kParts + part) * L::kTile + off) >> 4), id_s,
                          part > 0 || k > 0);
             }
           tc_commit(&s_full[half]);
-        }
-        __syncwarp();
-      };
-      auto values = [&](int half, uint32_t stage, bool first) {
-        if (elect_one()) {
-          const uint32_t va = smem_u32(smem + L::kV + stage * L::kTile);
+        };
+        auto values = [&](int half, uint32_t stage, bool first) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 64 + 8 * k,
-                       make_sdesc(va + k * 2048, L::kPanel, 1024, kSwizzle128B), id_o, !first || k > 0);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
-      while (more) {
-        const int halves = w.rt * RT + 128 < w.req.n * p.rep.d ? 2 : 1;
-        bool ok = true;
-        for (int i = 0; i < halves && ok; ++i) ok = wait(&q_full[i], qf[i]++ & 1);
-        ok = ok && wait(&k_full[tile % L::kKStages], (tile / L::kKStages) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        for (int i = 0; i < halves; ++i) scores(i, tile % L::kKStages);
-        commit(&k_empty[tile % L::kKStages]);
-        for (int j = 0; j < w.here && ok; ++j, ++tile) {
-          const bool next = j + 1 < w.here;
-          const uint32_t ks = (tile + 1) % L::kKStages, vs = tile % L::kVStages;
+            mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * k, vd + ((stage * L::kTile + k * 2048) >> 4), id_o, !first || k > 0);
+        };
+        while (more && ok) {
+          const int halves = w.rt * RT + 128 < w.req.n * p.rep.d ? 2 : 1;
+          ok = wait1(&k_full[tile % L::kKStages], (tile / L::kKStages) & 1);
           for (int i = 0; i < halves && ok; ++i) {
-            ok = wait(&p_full[i], pf[i]++ & 1);
-            if (ok && i == 0) ok = wait(&v_full[vs], (tile / L::kVStages) & 1);
+            ok = wait1(&q_full[i], qf[i]++ & 1);
             if (!ok) break;
             tc_fence_after();
-            values(i, vs, j == 0);
-            if (next) {
-              if (i == 0) {
-                ok = wait(&k_full[ks], ((tile + 1) / L::kKStages) & 1);
+            scores(i, tile % L::kKStages);
+          }
+          if (!ok) break;
+          tc_commit(&k_empty[tile % L::kKStages]);
+          for (int j = 0; j < w.here && ok; ++j, ++tile) {
+            const bool next = j + 1 < w.here;
+            const uint32_t ks = (tile + 1) % L::kKStages, vs = tile % L::kVStages;
+            // what the code warps bring is there long before the weights
+            ok = wait1(&v_full[vs], (tile / L::kVStages) & 1) &&
+                 (!next || L::kKStages == 1 || wait1(&k_full[ks], ((tile + 1) / L::kKStages) & 1));
+            for (int i = 0; i < halves && ok; ++i) {
+              ok = wait1(&p_full[i], pf[i]++ & 1);
+              if (!ok) break;
+              tc_fence_after();
+              values(i, vs, j == 0);
+              if (L::kKStages == 1 && next && i == 0) {   // a single stage is filled behind the scores before it
+                ok = wait1(&k_full[ks], ((tile + 1) / L::kKStages) & 1);
                 if (!ok) break;
                 tc_fence_after();
               }
-              scores(i, ks);
-            } else {
-              commit(&o_full[i]);
+              if (next)
+                scores(i, ks);
+              else
+                tc_commit(&o_full[i]);
             }
+            if (!ok) break;
+            tc_commit(&v_empty[vs]);
+            if (next) tc_commit(&k_empty[ks]);
           }
-          if (!ok) break;
-          commit(&v_empty[vs]);
-          if (next) commit(&k_empty[ks]);
+          more = ok && walk_next<RT, KT>(p, w);
         }
-        if (!ok) break;
-        more = walk_next<RT, KT>(p, w);
+        tc_commit(mma_done);
       }
+      __syncwarp();
       // everything issued has retired before TMEM is released
-      commit(mma_done);
       if (!warp_wait(mma_done, 0, drain_budget(budget), nullptr) && lane == 0) raise_error(kErrWaitAttn);
     }
   }
