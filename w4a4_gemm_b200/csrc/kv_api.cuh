@@ -120,6 +120,23 @@ int kv_geometry(const svdq_kv_cache* c, KvGeom* g, bool need_pool) {
   return SVDQ_OK;
 }
 
+using NormKernel = void (*)(NormRopeParams);
+
+template <int LANES>
+NormKernel norm_kernel_of(bool interleaved, bool batched) {
+  if (interleaved) return batched ? qk_norm_rope_kernel<LANES, true, kNormBatch> : qk_norm_rope_kernel<LANES, true, 1>;
+  return batched ? qk_norm_rope_kernel<LANES, false, kNormBatch> : qk_norm_rope_kernel<LANES, false, 1>;
+}
+NormKernel norm_kernel(int lanes_log2, bool interleaved, bool batched) {
+  switch (lanes_log2) {
+    case 1: return norm_kernel_of<2>(interleaved, batched);
+    case 2: return norm_kernel_of<4>(interleaved, batched);
+    case 3: return norm_kernel_of<8>(interleaved, batched);
+    case 4: return norm_kernel_of<16>(interleaved, batched);
+    default: return norm_kernel_of<32>(interleaved, batched);
+  }
+}
+
 // rows of heads x D bf16 values whose loads are whole 16-byte words
 bool rows_ok(const void* p, long long stride) { return p != nullptr && aligned16(p) && stride % 8 == 0 && stride >= 0; }
 
@@ -181,7 +198,7 @@ SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* d, void* stream) {
     return SVDQ_ERR_INVALID_ARG;
   if (d->k_heads > 0 && (!rows_ok(d->k, d->k_stride) || !rows_ok(d->k_out, d->k_out_stride) || (d->rows > 1 && d->k_out_stride < kn)))
     return SVDQ_ERR_INVALID_ARG;
-  if (d->rot_dim > 0 && (d->table == nullptr || d->table_rows < 0)) return SVDQ_ERR_INVALID_ARG;
+  if (d->rot_dim > 0 && (d->table == nullptr || !aligned16(d->table) || d->table_rows < 0)) return SVDQ_ERR_INVALID_ARG;
   if (d->rot_dim > 0 && d->positions == nullptr && d->table_rows < d->rows) return SVDQ_ERR_INVALID_ARG;
   if ((d->q_weight != nullptr && !aligned16(d->q_weight)) || (d->k_weight != nullptr && !aligned16(d->k_weight))) return SVDQ_ERR_INVALID_ARG;
   if (d->norm && !(d->eps >= 0.f)) return SVDQ_ERR_INVALID_ARG;
@@ -210,15 +227,19 @@ SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* d, void* stream) {
   p.norm = d->norm != 0;
   p.interleaved = d->interleaved != 0;
   p.eps = d->eps;
-  p.lanes_log2 = log2_exact((d->head_dim + 7) / 8);
+  const int lanes_log2 = log2_exact((d->head_dim + 7) / 8);   // of a head
   const int heads = d->q_heads + d->k_heads;
-  p.chunk = 1;
-  p.chunks = heads;
-  const long long threads = (static_cast<long long>(d->rows) * p.chunks) << p.lanes_log2;
-  const long long ctas = (threads + kNormThreads - 1) / kNormThreads;
-  if (ctas > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  SVDQ_CUDA(launch_pdl(qk_norm_rope_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), 0,
-                       static_cast<cudaStream_t>(stream), 0u, p));
+  // Heads that a lane group walks: as many as leave two waves of resident warps (64 per SM), at most 16; each row's
+  // cosines and sines are then loaded once per chunk.  Few rows take a head per group: latency counts there.
+  const long long lanes = static_cast<long long>(d->rows) << lanes_log2;
+  const long long want = static_cast<long long>(g_dev[dev].sms) * 2048 * 2;
+  p.chunk = static_cast<int>(std::max<long long>(1, std::min<long long>(16, lanes * heads / want)));
+  if (p.chunk >= kNormBatch) p.chunk = p.chunk / kNormBatch * kNormBatch;
+  p.chunks = (heads + p.chunk - 1) / p.chunk;
+  const long long ctas = (lanes * p.chunks + kNormThreads - 1) / kNormThreads;
+  if (ctas * kNormThreads > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  SVDQ_CUDA(launch_pdl(norm_kernel(lanes_log2, p.interleaved, p.chunk >= kNormBatch), dim3(static_cast<unsigned>(ctas)),
+                       dim3(kNormThreads), 0, static_cast<cudaStream_t>(stream), 0u, p));
   return SVDQ_OK;
 }
 

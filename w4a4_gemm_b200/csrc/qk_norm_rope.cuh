@@ -24,6 +24,7 @@
 namespace svdq {
 
 constexpr int kNormThreads = 128;
+constexpr int kNormBatch = 2;
 
 struct NormRopeParams {
   const __nv_bfloat16* q;
@@ -39,32 +40,100 @@ struct NormRopeParams {
   int rows, q_heads, k_heads, D, rot;
   int norm, interleaved;
   float eps;
-  int lanes_log2;                  // log2 of the lanes of a head
   int chunk;                       // heads that a lane group walks
   int chunks;                      // lane groups per row
 };
 
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& a, float* v) {
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& a, float2* v) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+
+// `n` heads from `src` to `dst` (D elements apart; this lane's 8 elements of each); `n_warp` is the largest n in the warp.
+//   out = r (x A + x' B): x' the partner of x in its pair, A = w cos, B = -+ w' sin, r the head's 1 / rms.
+// A and B do not depend on the head, only on the row and on whether it is a query or a key.  BATCH heads
+// are loaded before the first is used.
+template <int LANES, bool INTERLEAVED, int BATCH>
+__device__ __forceinline__ void norm_rope_heads(const NormRopeParams& p, const __nv_bfloat16* src, __nv_bfloat16* dst, int n, int n_warp,
+                                                const __nv_bfloat16* w, bool mine, bool rotated, int l, int partner,
+                                                const float2 (&cs)[4], const float2 (&sn)[4]) {
+  float2 A[4], B[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = B[i] = make_float2(1.f, 1.f);
+  if (p.norm && w != nullptr && mine) {
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * l)), A);
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * partner)), B);
+    if (INTERLEAVED) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) B[i] = make_float2(B[i].y, B[i].x);
+    }
+  }
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
+    A[i] = fmul2_rn(A[i], cs[i]);
+    B[i] = fmul2_rn(B[i], sn[i]);
+  }
+  const float inv_d = 1.f / static_cast<float>(p.D);
+  for (int j = 0; j < n_warp; j += BATCH, src += BATCH * p.D, dst += BATCH * p.D) {
+    uint4 raw[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+      raw[b] = mine && j + b < n ? *reinterpret_cast<const uint4*>(src + b * p.D) : make_uint4(0u, 0u, 0u, 0u);
+    float ss[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      float2 x[4];
+      bf16x8_to_f32(raw[b], x);
+      float2 s2 = fmul2_rn(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) s2 = ffma2(x[i], x[i], s2);
+      ss[b] = s2.x + s2.y;
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o *= 2)
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) ss[b] += __shfl_xor_sync(0xffffffffu, ss[b], o);
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      uint4 other;
+      if (INTERLEAVED) {
+        other = make_uint4(__byte_perm(raw[b].x, 0, 0x1032), __byte_perm(raw[b].y, 0, 0x1032), __byte_perm(raw[b].z, 0, 0x1032),
+                           __byte_perm(raw[b].w, 0, 0x1032));
+      } else {
+        other.x = __shfl_sync(0xffffffffu, raw[b].x, partner, LANES);
+        other.y = __shfl_sync(0xffffffffu, raw[b].y, partner, LANES);
+        other.z = __shfl_sync(0xffffffffu, raw[b].z, partner, LANES);
+        other.w = __shfl_sync(0xffffffffu, raw[b].w, partner, LANES);
+      }
+      if (!rotated) other = make_uint4(0u, 0u, 0u, 0u);     // those elements keep their values, infinities included
+      const float r = p.norm ? rsqrtf(ss[b] * inv_d + p.eps) : 1.f;
+      const float2 r2 = make_float2(r, r);
+      float2 x[4], y[4];
+      bf16x8_to_f32(raw[b], x);
+      bf16x8_to_f32(other, y);
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = fmul2_rn(ffma2(x[i], A[i], fmul2_rn(y[i], B[i])), r2);
+        o[i] = pack_bf16x2(t.x, t.y);
+      }
+      if (mine && j + b < n) *reinterpret_cast<uint4*>(dst + b * p.D) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
-__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormRopeParams p) {
+template <int LANES, bool INTERLEAVED, int BATCH>
+__global__ void __launch_bounds__(kNormThreads, 8) qk_norm_rope_kernel(const NormRopeParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int L = 1 << p.lanes_log2;
-  const long long group = (static_cast<long long>(blockIdx.x) * kNormThreads + threadIdx.x) >> p.lanes_log2;
-  const int l = threadIdx.x & (L - 1);
-  const long long row = group / p.chunks;
-  const int h0 = static_cast<int>(group % p.chunks) * p.chunk;
-  const int heads = p.q_heads + p.k_heads;
+  const int group = static_cast<int>(blockIdx.x * kNormThreads + threadIdx.x) / LANES;
+  const int l = threadIdx.x & (LANES - 1);
+  const int row = group / p.chunks;
+  const int h0 = (group - row * p.chunks) * p.chunk, h1 = min(h0 + p.chunk, p.q_heads + p.k_heads);
   // A padded row (position below 0) is left as it is; every lane stays for the shuffles.
   bool ok = row < p.rows;
-  long long pos = row;
+  int pos = row;
   if (ok && p.positions != nullptr) pos = p.positions[row];
   if (ok && pos >= p.table_rows && p.rot > 0) {
     if (l == 0) raise_error(kErrIndex);
@@ -75,82 +144,46 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const NormRo
 
   const int half = p.rot / 2;
   const bool rotated = 8 * l < p.rot;
-  float cs[8], sn[8];
+  const int partner = (rotated && !INTERLEAVED) ? (8 * l < half ? l + half / 8 : l - half / 8) : l;
+  float2 cs[4], sn[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    cs[i] = make_float2(1.f, 1.f);
+    sn[i] = make_float2(0.f, 0.f);
   }
   if (mine && rotated) {
-    const float* t = p.table + pos * p.rot;
-    if (p.interleaved) {                     // 4 pairs of this lane
+    const float* t = p.table + static_cast<long long>(pos) * p.rot;
+    if (INTERLEAVED) {                       // 4 pairs of this lane
+      const float4 c = __ldg(reinterpret_cast<const float4*>(t + 4 * l)), s = __ldg(reinterpret_cast<const float4*>(t + half + 4 * l));
+      const float cc[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        cs[2 * i] = cs[2 * i + 1] = __ldg(t + 4 * l + i);
-        const float s = __ldg(t + half + 4 * l + i);
-        sn[2 * i] = -s;
-        sn[2 * i + 1] = s;
+        cs[i] = make_float2(cc[i], cc[i]);
+        sn[i] = make_float2(-s4[i], s4[i]);
       }
     } else {                                 // 8 pairs, their other halves in the partner lane
-      const int i0 = (8 * l) % half;
       const bool second = 8 * l >= half;
+      const float* t0 = t + 8 * l - (second ? half : 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[i] = __ldg(t + i0 + i);
-        const float s = __ldg(t + half + i0 + i);
-        sn[i] = second ? s : -s;
+      for (int i = 0; i < 2; ++i) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(t0 + 4 * i)), s = __ldg(reinterpret_cast<const float4*>(t0 + half + 4 * i));
+        cs[2 * i] = make_float2(c.x, c.y);
+        cs[2 * i + 1] = make_float2(c.z, c.w);
+        sn[2 * i] = second ? make_float2(s.x, s.y) : make_float2(-s.x, -s.y);
+        sn[2 * i + 1] = second ? make_float2(s.z, s.w) : make_float2(-s.z, -s.w);
       }
     }
   }
-  const int partner = (rotated && !p.interleaved) ? (8 * l < half ? l + half / 8 : l - half / 8) : l;
-  const float inv_d = 1.f / static_cast<float>(p.D);
-
-  for (int j = 0; j < p.chunk; ++j) {
-    const int h = h0 + j;
-    const bool is_q = h < p.q_heads;
-    const int hh = is_q ? h : h - p.q_heads;
-    const bool act = mine && h < heads;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (act) {
-      const __nv_bfloat16* src = (is_q ? p.q + row * p.q_stride : p.k + row * p.k_stride) + hh * p.D + 8 * l;
-      bf16x8_to_f32(*reinterpret_cast<const uint4*>(src), x);
-    }
-    if (p.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      for (int o = 1; o < L; o *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * inv_d + p.eps);
-      const __nv_bfloat16* w = is_q ? p.q_weight : p.k_weight;
-      float wf[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wf[i] = 1.f;
-      if (act && w != nullptr) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * l)), wf);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
-    }
-    float y[8];
-    if (p.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner, L);
-    }
-    if (act) {
-      if (rotated) {                         // the others keep their values, infinities included
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
-      }
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-      __nv_bfloat16* dst = (is_q ? p.q_out + row * p.q_out_stride : p.k_out + row * p.k_out_stride) + hh * p.D + 8 * l;
-      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
+  // The bounds of the loops are those of the whole warp: its shuffles need every lane.
+  const int nq = max(0, min(h1, p.q_heads) - h0), k0 = max(h0, p.q_heads), nk = max(0, h1 - k0);
+  const int nq_warp = LANES == 32 ? nq : __reduce_max_sync(0xffffffffu, nq), nk_warp = LANES == 32 ? nk : __reduce_max_sync(0xffffffffu, nk);
+  if (nq_warp > 0)
+    norm_rope_heads<LANES, INTERLEAVED, BATCH>(p, p.q + row * p.q_stride + h0 * p.D + 8 * l, p.q_out + row * p.q_out_stride + h0 * p.D + 8 * l,
+                                               nq, nq_warp, p.q_weight, mine, rotated, l, partner, cs, sn);
+  if (nk_warp > 0)
+    norm_rope_heads<LANES, INTERLEAVED, BATCH>(p, p.k + row * p.k_stride + (k0 - p.q_heads) * p.D + 8 * l,
+                                               p.k_out + row * p.k_out_stride + (k0 - p.q_heads) * p.D + 8 * l, nk, nk_warp, p.k_weight,
+                                               mine, rotated, l, partner, cs, sn);
 }
 
 }  // namespace svdq
