@@ -101,15 +101,19 @@ def test_refused_attentions(S):
 
 
 def test_python_refusals_without_a_gpu(S):
-    """CPU tensors, wrong types and shapes never reach the library."""
+    """CPU tensors and wrong formats never reach the library."""
     with pytest.raises(TypeError):
         S.KVCache("nvfp4", 2, 64, 16, torch.zeros(1, 2, 1152, dtype=torch.uint8))
     with pytest.raises(S.SvdqError):
-        S.KVCache("nvfp4", 2, 80, 16)
+        S.KVCache("nvfp4", 2, 80, 16, num_pages=1)
     with pytest.raises(S.SvdqError):
-        S.KVCache("w8a8", 2, 64, 16)
+        S.KVCache("w8a8", 2, 64, 16, num_pages=1)
     with pytest.raises(KeyError):
         S.KVCache("fp8", 2, 64, 16)
+    with pytest.raises(TypeError):
+        S.KVCache("nvfp4", 2.5, 64, 16, num_pages=1)
+    with pytest.raises(TypeError):
+        S._ext().kv_append(b"not a cache", None, None, None)          # too few arguments
 
 
 def test_reference_plan_by_hand():

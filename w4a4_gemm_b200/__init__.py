@@ -407,79 +407,30 @@ def svdq_set_gemm_raster(group_m: int = 0):
 
 
 # ------------------------------------------- attention over a 4-bit cache ---
-# These calls run once per layer and decode step, so the checks stay cheap: one
-# pass over the arguments, no allocation but the outputs, the argument block by
-# reference.
+# These calls run once per layer and decode step, so they go through the compiled
+# module svdq_torch (csrc/svdq_torch.cpp), which checks the tensors, allocates the
+# outputs and calls the C entry points in one step: ctypes and Python checks cost
+# about 20 us a call, the module 4 to 6 us, launch included.
 
-_LAUNCH = None      # torch's raw-stream lookup: the address of the current stream without a Stream object
-
-
-def _launch_stream(stream, dev: int) -> int:
-    global _LAUNCH
-    if stream is not None:
-        return stream.cuda_stream
-    if _LAUNCH is None:
-        _LAUNCH = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return _LAUNCH(dev)
+_fast = None
 
 
-def _here(t, dtype, name: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t
+def _ext():
+    """The compiled module; raises if it has not been built."""
+    global _fast
+    if _fast is None:
+        lib()
+        try:
+            from . import svdq_torch
+        except ImportError as e:
+            raise RuntimeError(f"the svdq_torch module is missing or does not load ({e}): "
+                               "build it with `python -m w4a4_gemm_b200.build`") from e
+        _fast = svdq_torch
+    return _fast
 
 
-def _array(t, dtype, name: str, dev: int, n: Optional[int] = None) -> int:
-    """Address of a contiguous vector on the launch device."""
-    _here(t, dtype, name)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must have shape ({'n' if n is None else n},), got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return t.data_ptr()
-
-
-def _rows(t, name: str, dev: int, rows: int, heads: int, dim: int):
-    """(address, row stride) of rows x heads x dim bf16 whose heads are contiguous in a row."""
-    _here(t, torch.bfloat16, name)
-    if t.dim() != 3 or tuple(t.shape) != (rows, heads, dim):
-        raise ValueError(f"{name} must have shape {(rows, heads, dim)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if rows <= 1:
-        s0 = heads * dim
-    if s0 % 8 or t.data_ptr() % 16:
-        raise ValueError(f"{name}: rows must start on 16-byte boundaries")
-    return t.data_ptr(), s0
-
-
-def _table(block_table, dev: int):
-    _here(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be batch x pages")
-    if block_table.get_device() != dev:
-        raise ValueError(f"block_table is on cuda:{block_table.get_device()}, the current device is cuda:{dev}")
-    b, w = block_table.shape
-    s0, s1 = block_table.stride()
-    if b and ((w > 1 and s1 != 1) or (b > 1 and s0 < w)):
-        raise ValueError("block_table: the pages of a request must be contiguous, and its rows must not overlap")
-    return block_table.data_ptr(), (s0 if b > 1 else w), b, w
-
-
-def _empty(shape, dtype, device, stream):
-    """An output allocated for the stream that the kernel runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 class KVCache:
@@ -489,58 +440,37 @@ class KVCache:
     one of `num_pages` pages is allocated on `device` (its contents are whatever
     the memory held: tokens that were never appended are never read)."""
 
+    __slots__ = ("fmt", "kv_heads", "head_dim", "page_size", "pool", "num_pages", "page_bytes", "_c")
+
     def __init__(self, fmt, kv_heads: int, head_dim: int, page_size: int, pool: Optional[torch.Tensor] = None,
                  num_pages: Optional[int] = None, device=None):
-        self.fmt, self.kv_heads, self.head_dim, self.page_size = _FMT[fmt], int(kv_heads), int(head_dim), int(page_size)
-        self._c = _KvCache(self.fmt, self.kv_heads, self.head_dim, self.page_size, 0, None)
-        self._ref = ctypes.byref(self._c)
-        n = ctypes.c_size_t()
-        _check(lib().svdq_kv_page_bytes(self._ref, ctypes.byref(n)), "svdq_kv_page_bytes")
-        self.page_bytes = n.value
-        block = self.page_bytes // self.kv_heads
+        self.fmt, self.kv_heads, self.head_dim, self.page_size = _FMT[fmt], kv_heads, head_dim, page_size
+        fast = _fast or _ext()
         if pool is None:
-            pool = torch.empty((int(num_pages), self.kv_heads, block), dtype=torch.uint8,
+            r = fast.cache(self.fmt, kv_heads, head_dim, page_size, None)
+            if type(r) is int:
+                _check(r, "KVCache")
+            if num_pages is None:
+                raise ValueError("KVCache needs a pool or num_pages")
+            pool = torch.empty((int(num_pages), kv_heads, r[1] // kv_heads), dtype=torch.uint8,
                                device=device or torch.device("cuda", torch.cuda.current_device()))
-        _here(pool, torch.uint8, "pool")
-        if pool.dim() != 3 or pool.shape[1] != self.kv_heads or pool.shape[2] != block or not pool.is_contiguous():
-            raise ValueError(f"pool must be contiguous, [pages, {self.kv_heads}, {block}], got {tuple(pool.shape)}")
-        if pool.data_ptr() % 16:
-            raise ValueError("pool must start on a 16-byte boundary")
-        self.pool, self.num_pages, self.device_index = pool, pool.shape[0], pool.get_device()
-        self._c.num_pages, self._c.pool = self.num_pages, pool.data_ptr()
-
-    def _on(self) -> int:
-        dev = torch.cuda.current_device()
-        if dev != self.device_index:
-            raise ValueError(f"the cache is on cuda:{self.device_index}, the current device is cuda:{dev}")
-        return dev
+        r = fast.cache(self.fmt, kv_heads, head_dim, page_size, pool)
+        if type(r) is int:
+            _check(r, "KVCache")
+        self._c, self.page_bytes = r
+        self.pool, self.num_pages = pool, pool.shape[0]
 
 
 def svdq_kv_plan(q_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
                  rows: int, page_size: int, stream=None):
     """(cu_q, total_lens, positions, slots, used) of a batch that brings q_lens[b] tokens behind
-    kv_lens[b] cached ones; enters the pages that it opens into block_table.  `rows` may be more
-    than the sum of q_lens: the rows behind it get position and slot -1 (see include/svdq.h)."""
-    dev = torch.cuda.current_device()
-    table, stride, batch, width = _table(block_table, dev)
-    ql, kl = _array(q_lens, torch.int32, "q_lens", dev, batch), _array(kv_lens, torch.int32, "kv_lens", dev, batch)
-    free = _array(free_pages, torch.int32, "free_pages", dev)
-    rows = int(rows)
-    if rows < 0:
-        raise ValueError("rows must not be negative")
-    # one allocation for the 32-bit results, each at a 16-byte boundary
-    pad = lambda n: (n + 3) & ~3  # noqa: E731
-    o_total, o_used = pad(batch + 1), pad(batch + 1) + pad(batch)
-    o_pos = o_used + 4
-    ints = _empty((o_pos + rows,), torch.int32, block_table.device, stream)
-    slots = _empty((rows,), torch.int64, block_table.device, stream)
-    base = ints.data_ptr()
-    d = _KvPlanDesc(ql, kl, table, stride, width, free, free_pages.shape[0], batch, rows, int(page_size), base,
-                    base + 4 * o_total, base + 4 * o_pos, slots.data_ptr(), base + 4 * o_used)
-    rc = lib().svdq_kv_plan(ctypes.byref(d), _launch_stream(stream, dev))
-    if rc:
-        _check(rc, "svdq_kv_plan")
-    return ints[:batch + 1], ints[o_total:o_total + batch], ints[o_pos:], slots, ints[o_used:o_used + 1]
+    kv_lens[b] cached ones (int32); enters the pages that it opens into block_table (int32 batch x
+    pages).  `rows` may be more than the sum of q_lens: the rows behind it get position and slot -1
+    (see include/svdq.h)."""
+    r = (_fast or _ext()).kv_plan(q_lens, kv_lens, block_table, free_pages, rows, page_size, _handle(stream))
+    if type(r) is int:
+        _check(r, "svdq_kv_plan")
+    return r
 
 
 def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, table: Optional[torch.Tensor] = None,
@@ -550,78 +480,39 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, table: Optional[torch.Te
                       k_out: Optional[torch.Tensor] = None, stream=None):
     """Norm and rotate query and key heads (see include/svdq.h): q rows x q_heads x dim and
     k rows x k_heads x dim bf16 (views of the QKV projection's rows, for instance), table
-    positions x rot_dim fp32 cosines and sines.  Returns (q_out, k_out); pass q and k themselves
-    to work in place."""
-    dev = torch.cuda.current_device()
-    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 3 or k.dim() != 3:
-        raise TypeError("q and k must be rows x heads x dim tensors")
-    rows, hq, dim = q.shape
-    hk = k.shape[1]
-    qp, qs = _rows(q, "q", dev, rows, hq, dim)
-    kp, ks = _rows(k, "k", dev, rows, hk, dim)
-    if q_out is None:
-        q_out = _empty((rows, hq, dim), torch.bfloat16, q.device, stream)
-    if k_out is None:
-        k_out = _empty((rows, hk, dim), torch.bfloat16, q.device, stream)
-    qop, qos = _rows(q_out, "q_out", dev, rows, hq, dim)
-    kop, kos = _rows(k_out, "k_out", dev, rows, hk, dim)
-    tp, tr, rot = None, 0, 0
-    if table is not None:
-        _here(table, torch.float32, "table")
-        if table.dim() != 2 or not table.is_contiguous() or table.get_device() != dev:
-            raise ValueError("table must be a contiguous positions x rot_dim tensor on the current device")
-        tp, (tr, rot) = table.data_ptr(), table.shape
-    d = _QkNormRopeDesc(qp, kp, qop, kop, qs, ks, qos, kos,
-                        None if q_weight is None else _array(q_weight, torch.bfloat16, "q_weight", dev, dim),
-                        None if k_weight is None else _array(k_weight, torch.bfloat16, "k_weight", dev, dim), tp,
-                        None if positions is None else _array(positions, torch.int32, "positions", dev, rows), tr, rows,
-                        hq, hk, dim, rot, int(norm), int(interleaved), eps)
-    rc = lib().svdq_qk_norm_rope(ctypes.byref(d), _launch_stream(stream, dev))
-    if rc:
-        _check(rc, "svdq_qk_norm_rope")
-    return q_out, k_out
+    positions x rot_dim fp32 cosines and sines, positions int32 rows.  Returns (q_out, k_out); pass
+    q and k themselves to work in place."""
+    r = (_fast or _ext()).qk_norm_rope(q, k, table, positions, q_weight, k_weight, eps, norm, interleaved, q_out, k_out,
+                                       _handle(stream))
+    if type(r) is int:
+        _check(r, "svdq_qk_norm_rope")
+    return r
 
 
 def svdq_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
     """Quantize k and v (bf16 rows x kv_heads x head_dim) into the cache at `slots` (int64 rows;
     below 0: a padded row, skipped)."""
-    dev = cache._on()
-    sp = _array(slots, torch.int64, "slots", dev)
-    rows = slots.shape[0]
-    kp, ks = _rows(k, "k", dev, rows, cache.kv_heads, cache.head_dim)
-    vp, vs = _rows(v, "v", dev, rows, cache.kv_heads, cache.head_dim)
-    rc = lib().svdq_kv_append(cache._ref, kp, vp, ks, vs, sp, rows, _launch_stream(stream, dev))
-    if rc:
-        _check(rc, "svdq_kv_append")
+    r = (_fast or _ext()).kv_append(cache._c, k, v, slots, _handle(stream))
+    if type(r) is int:
+        _check(r, "svdq_kv_append")
 
 
 def svdq_kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, stream=None):
     """(k, v) rows x kv_heads x head_dim: the values held at `slots`, in bf16 or fp32."""
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-    dev = cache._on()
-    sp = _array(slots, torch.int64, "slots", dev)
-    rows = slots.shape[0]
-    k = _empty((rows, cache.kv_heads, cache.head_dim), dtype, slots.device, stream)
-    v = _empty((rows, cache.kv_heads, cache.head_dim), dtype, slots.device, stream)
-    rc = lib().svdq_kv_read(cache._ref, sp, rows, int(dtype is torch.float32), k.data_ptr(), v.data_ptr(),
-                            _launch_stream(stream, dev))
-    if rc:
-        _check(rc, "svdq_kv_read")
-    return k, v
-
-
-def _attention_desc(cache, q_ptr, q_stride, out_ptr, out_stride, lse, cu_q, kv_lens, table, stride, width, batch, rows,
-                    heads, causal, window, scale):
-    return _KvAttentionDesc(cache._c, q_ptr, q_stride, out_ptr, out_stride, lse, cu_q, kv_lens, table, stride, width,
-                            batch, rows, heads, int(causal), int(window), scale, None)
+    r = (_fast or _ext()).kv_read(cache._c, slots, dtype is torch.float32, _handle(stream))
+    if type(r) is int:
+        _check(r, "svdq_kv_read")
+    return r
 
 
 def svdq_kv_attention_workspace_bytes(cache: KVCache, q_heads: int, rows: int, batch: int) -> int:
-    d = _attention_desc(cache, None, 0, None, 0, None, None, None, None, 0, 0, int(batch), int(rows), int(q_heads), 0, 0, 1.0)
-    n = ctypes.c_size_t()
-    _check(lib().svdq_kv_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n)), "svdq_kv_attention_workspace_bytes")
-    return n.value
+    """Bytes of the workspace of svdq_kv_attention for these sizes."""
+    r = (_fast or _ext()).kv_attention_workspace_bytes(cache._c, q_heads, rows, batch)
+    if type(r) is tuple:
+        _check(r[0], "svdq_kv_attention_workspace_bytes")
+    return r
 
 
 def svdq_kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor,
@@ -631,35 +522,8 @@ def svdq_kv_attention(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor, kv_le
     """Attention of q (bf16 rows x q_heads x head_dim) over the cache; scale 1 / sqrt(head_dim)
     unless given.  Returns out, or (out, lse) with lse fp32 rows x q_heads (see include/svdq.h).
     Without a workspace one is allocated for the call."""
-    dev = cache._on()
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise TypeError("q must be a rows x heads x dim tensor")
-    rows, heads, dim = q.shape
-    if dim != cache.head_dim:
-        raise ValueError(f"q has head_dim {dim}, the cache has {cache.head_dim}")
-    qp, qs = _rows(q, "q", dev, rows, heads, dim)
-    table, stride, batch, width = _table(block_table, dev)
-    if out is None:
-        out = _empty((rows, heads, dim), torch.bfloat16, q.device, stream)
-    op, os_ = _rows(out, "out", dev, rows, heads, dim)
-    lse = _empty((rows, heads), torch.float32, q.device, stream) if return_lse else None
-    d = _attention_desc(cache, qp, qs, op, os_, None if lse is None else lse.data_ptr(),
-                        _array(cu_q, torch.int32, "cu_q", dev, batch + 1),
-                        _array(kv_lens, torch.int32, "kv_lens", dev, batch), table, stride, width, batch, rows, heads,
-                        causal, window, dim ** -0.5 if scale is None else scale)
-    n = ctypes.c_size_t()
-    rc = lib().svdq_kv_attention_workspace_bytes(ctypes.byref(d), ctypes.byref(n))
-    if rc:
-        _check(rc, "svdq_kv_attention")
-    if n.value:
-        if workspace is None:
-            workspace = _empty((n.value,), torch.uint8, q.device, stream)
-        else:
-            _array(workspace, torch.uint8, "workspace", dev)
-            if workspace.shape[0] < n.value:
-                raise ValueError("workspace too small")
-        d.workspace = workspace.data_ptr()
-    rc = lib().svdq_kv_attention(ctypes.byref(d), _launch_stream(stream, dev))
-    if rc:
-        _check(rc, "svdq_kv_attention")
-    return (out, lse) if return_lse else out
+    r = (_fast or _ext()).kv_attention(cache._c, q, cu_q, kv_lens, block_table, scale, causal, window, out, return_lse,
+                                       workspace, _handle(stream))
+    if type(r) is int:
+        _check(r, "svdq_kv_attention")
+    return r
