@@ -664,22 +664,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12) {
       // ---------------------------------------------------------------- MMA
-      // One lane waits and issues; the others meet it behind the loop.
-      if (lane == 0) {
+      // The whole warp waits, one lane issues: descriptors then live in uniform registers (with one lane in the whole
+      // loop an MMA took 80 to 120 cycles to issue, against 64 on the tensor core).
+      {
         constexpr uint32_t id_s = idesc_f16_f32(128, KT, false), id_o = idesc_f16_f32(128, D, true);
         uint32_t tile = 0, pf[2] = {0, 0}, qf[2] = {0, 0};
         Walk w = walk_start<RT, KT>(p, share);
         bool more = w.count > 0, ok = true;
         const uint64_t qd = make_kmajor_desc(smem_u32(smem + L::kQ), 128), kd = make_kmajor_desc(smem_u32(smem + L::kK), 128);
         const uint64_t vd = make_sdesc(smem_u32(smem + L::kV), L::kPanel, 1024, kSwizzle128B);
-        auto wait1 = [&](uint64_t* bar, uint32_t parity) {
-          if (mbar_wait(bar, parity, budget, const_cast<int*>(abort_flag))) return true;
-          if (!*abort_flag) raise_error(kErrWaitAttn);
-          *abort_flag = 1;
-          return false;
+        auto& wait1 = wait;
+        auto commit = [&](uint64_t* bar) {
+          if (elect_one()) tc_commit(bar);
+          __syncwarp();
         };
         // descriptors count addresses in 16 bytes: offsets are added to the low word's field
         auto scores = [&](int half, uint32_t stage) {
+          if (elect_one()) {
 #pragma unroll
           for (int part = 0; part < L::kParts; ++part)
 #pragma unroll
@@ -689,11 +690,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
                          part > 0 || k > 0);
             }
           tc_commit(&s_full[half]);
+          }
+          __syncwarp();
         };
         auto values = [&](int half, uint32_t stage, bool first) {
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * k, vd + ((stage * L::kTile + k * 2048) >> 4), id_o, !first || k > 0);
+            for (int k = 0; k < KT / 16; ++k)
+              mma_f16_ts(tmem + 256 + 128 * half, tmem + 128 * half + 8 * k, vd + ((stage * L::kTile + k * 2048) >> 4), id_o, !first || k > 0);
+          }
+          __syncwarp();
         };
         while (more && ok) {
           const int halves = w.rt * RT + 128 < w.req.n * p.rep.d ? 2 : 1;
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
             scores(i, tile % L::kKStages);
           }
           if (!ok) break;
-          tc_commit(&k_empty[tile % L::kKStages]);
+          commit(&k_empty[tile % L::kKStages]);
           for (int j = 0; j < w.here && ok; ++j, ++tile) {
             const bool next = j + 1 < w.here;
             const uint32_t ks = (tile + 1) % L::kKStages, vs = tile % L::kVStages;
@@ -725,17 +731,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
               if (next)
                 scores(i, ks);
               else
-                tc_commit(&o_full[i]);
+                commit(&o_full[i]);
             }
             if (!ok) break;
-            tc_commit(&v_empty[vs]);
-            if (next) tc_commit(&k_empty[ks]);
+            commit(&v_empty[vs]);
+            if (next) commit(&k_empty[ks]);
           }
           more = ok && walk_next<RT, KT>(p, w);
         }
-        tc_commit(mma_done);
+        if (elect_one()) tc_commit(mma_done);
+        __syncwarp();
       }
-      __syncwarp();
       // everything issued has retired before TMEM is released
       if (!warp_wait(mma_done, 0, drain_budget(budget), nullptr) && lane == 0) raise_error(kErrWaitAttn);
     }
