@@ -10,13 +10,17 @@ Tolerances, per element (half a bf16 step is 2^-8 of the value, half an fp16 ste
                     products, the rotation's two products and one addition, the
                     table's own rounding: under 16 = 2^4 fp32 steps in all.
   attention         2^-8 |o| for the output, and relative to A = sum p |v| / sum p:
-                    2^-11 for the fp16 weights, 2^-40 sum |v| / sum p for the
-                    smallest of them (the largest weight is held as 2^15, the
-                    smallest fp16 step is 2^-24, so half of it is 2^-40 of the
-                    largest weight), 2 ds for the scores, 2^-20 for
+                    2^-11 for the fp16 weights, 2 ds for the scores, 2^-20 for
                     exp2 and the division, n 2^-23 for n keys' fp32 sums (a tensor
                     core may truncate: a whole step each), where ds, the error of
-                    a score, is (D + 8) 2^-23 max_t scale |q|.|k_t|.
+                    a score, is (D + 8) 2^-23 max_t scale |q|.|k_t|; then what fp16
+                    leaves of the smallest weights: the largest weight is held as 2^10 at
+                    least (the lazy maximum of the many-row kernel), the smallest
+                    fp16 step is 2^-24, half of it 2^-35 of the largest weight:
+                    2^-35 sum |v| / sum p.  INT4 adds 2^-11 A (values rounded to
+                    fp16 in the many-row kernel) and, as weights meet scales
+                    relative to the largest scale, 2^-25 max |v| (values below it) and
+                    n 2^-36 max |v| / sum p (weights: 2^-39 each, codes up to 7).
   lse               ds + 2^-20 (1 + |lse|) + n 2^-23 (its sum is taken in fp32, before the
                     weights are rounded).
 """
@@ -68,7 +72,7 @@ def store(pool, fmt, D, page, slots, k, v):
     return out
 
 
-def attention(q, keys, values, scale, causal, window):
+def attention(q, keys, values, scale, causal, window, int4=False):
     """One request: q [n, Hq, D], keys / values [kv, Hk, D] float64 -> out, lse, tolerances of both."""
     n, hq, D = q.shape
     kv, hk, _ = keys.shape
@@ -97,7 +101,10 @@ def attention(q, keys, values, scale, causal, window):
         A = w @ np.abs(v) / total[:, None]
         ds = (D + 8) * 2.0 ** -23 * big
         tol_o[:, h] += 2.0 ** -8 * np.abs(out[:, h]) + (2.0 ** -11 + 2 * ds + 2.0 ** -20 + kv * 2.0 ** -23)[:, None] * A
-        tol_o[:, h] += 2.0 ** -40 * (seen @ np.abs(v)) / total[:, None]
+        tol_o[:, h] += 2.0 ** -35 * (seen @ np.abs(v)) / total[:, None]
+        if int4:
+            most = np.abs(v).max()
+            tol_o[:, h] += 2.0 ** -11 * A + (2.0 ** -25 * most + 2.0 ** -36 * most * seen.sum(1) / total)[:, None]
         tol_l[:, h] += ds + 2.0 ** -20 * (1 + np.abs(np.where(any_, lse[:, h], 0))) + kv * 2.0 ** -23
     return out, lse, tol_o, tol_l
 
@@ -196,5 +203,5 @@ class Batch:
         parts = []
         for b, (n, kv) in enumerate(self.lens):
             q = self.q[self.cu[b]:self.cu[b + 1]].double().numpy()
-            parts.append(attention(q, self.keys[b], self.values[b], scale, causal, window))
+            parts.append(attention(q, self.keys[b], self.values[b], scale, causal, window, self.fmt == "int4"))
         return [np.concatenate([p[i] for p in parts]) for i in range(4)]

@@ -395,7 +395,7 @@ def test_serving_steps(S, fmt):
         for b, n in enumerate(new):
             for side, t in enumerate((k, v)):
                 held[b][side] = np.concatenate((held[b][side], R.quantize(fmt, t[at:at + n].cpu())[2]))
-            o, _, to, _ = R.attention(q[at:at + n].double().cpu().numpy(), *held[b], D ** -0.5, True, 0)
+            o, _, to, _ = R.attention(q[at:at + n].double().cpu().numpy(), *held[b], D ** -0.5, True, 0, fmt == "int4")
             within(out[at:at + n], o, to)
             at += n
         assert (out[at:] == 0).all()

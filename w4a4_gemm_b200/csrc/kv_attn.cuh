@@ -17,16 +17,17 @@
 // the few query rows its 8-column side.
 //   * FP4 formats: code * scale is exact in fp16 (2 + 4 significant bits), both for
 //     keys and values.
-//   * INT4: the codes are exact in fp16 and bf16.  A key group's scale multiplies
-//     its partial scores in fp32; a value group's scale multiplies the weights,
-//     which then span the range of fp16 scales times [0, 1], so they enter the
-//     product as a bf16 pair hi + lo (16 bits).
+//   * INT4: the codes are exact in fp16.  A key group's scale multiplies its partial
+//     scores in fp32; a value group's scale, divided by the power of two of the largest
+//     so far (a running exponent, like the running maximum), multiplies the weights
+//     before they are rounded to fp16.
 //   * Queries are bf16 and scores are products with fp16 keys: a row is divided by
 //     the power of two of its largest element, which leaves an exact fp16 value for
 //     every element down to 2^-17 of the largest and an error below 2^-36 of it
 //     for the rest.  The factor goes into the scores' scale.
-//   * Weights are exp2(x - max + 15), at most 2^15, so fp16 holds them to 2^-11
-//     relative down to 2^-29 of the largest and to 2^-40 absolute.
+//   * Weights are exp2(x - max + 15) (14 for INT4), so that they, times a scale
+//     below 2, end at 2^15 and fp16 holds them to 2^-11 relative down to 2^-29 of the
+//     largest (2^-28), to 2^-40 (2^-39) absolute.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,6 +47,8 @@ constexpr int kDecChunk = 64;                       // keys of a warp's step
 constexpr int kDecBlocks = kDecChunk / 16;
 constexpr int kDecUnit = kDecChunk * kDecWarps;     // keys of a unit of work
 constexpr int kDecStages = 2;
+// The weights are exp2(x - max + shift).
+__host__ __device__ constexpr float dec_shift(int fmt) { return fmt == kFmtInt4 ? 14.f : 15.f; }
 
 __host__ __device__ constexpr int dec_stage_bytes(int fmt, int D) {
   return 2 * kDecChunk * (D / 2 + kv_scale_bytes(fmt, D));
@@ -102,12 +105,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Eight 4-bit two's complement codes -> four fp16 pairs (code i, code i + 4): u = code ^ 8
-// under the exponent of 1024 is 1024 + u (or 1024 + 16 u), minus 1032 (or / 16, minus 72).
-__device__ __forceinline__ void int4x8_to_f16(uint32_t w, uint32_t* h) {
-  const uint32_t x = w ^ 0x88888888u, y = x >> 8;
-  const uint32_t p[4] = {(x & 0x000F000Fu) | 0x64006400u, (x & 0x00F000F0u) | 0x64006400u, (y & 0x000F000Fu) | 0x64006400u,
-                         (y & 0x00F000F0u) | 0x64006400u};
+// Four 4-bit two's complement codes of each half word -> four fp16 pairs, pair i from bits 4i of both halves: u =
+// code ^ 8 under the exponent of 1024 is 1024 + u (or 1024 + 16 u), minus 1032 (or / 16, minus 72).
+__device__ __forceinline__ void int4x8_to_f16(uint32_t x, uint32_t* h) {
+  const uint32_t y = x >> 8;
+  const uint32_t p[4] = {(x & 0x000F000Fu) ^ 0x64086408u, (x & 0x00F000F0u) ^ 0x64806480u, (y & 0x000F000Fu) ^ 0x64086408u,
+                         (y & 0x00F000F0u) ^ 0x64806480u};
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(p[i]), "r"(0x64086408u));                               // 1032
@@ -255,53 +258,41 @@ __device__ __forceinline__ void key_scores(const uint8_t* codes, const uint8_t* 
 }
 
 // O^T += V^T P^T for 16 keys.  w[nb][0..3]: the weights of this lane's score elements (keys of rows r and
-// r + 8, columns 2t and 2t + 1).  `usable`: keys below it are real, scales of the others count as zero.
+// r + 8, columns 2t and 2t + 1).  `usable`: keys below it are real, scales of the others count as zero (FP4).
+// INT4: `sc` holds the fp16 scales of the keys of rows r and r + 8, `down` the power of two that they are
+// divided by.
+__device__ __forceinline__ float int4_scale(uint32_t two, int g) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(g ? two >> 16 : two & 0xffffu)));
+}
 template <int FMT, int D, int NB, bool WHOLE>
-__device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* scales, int r, int t, int usable,
-                                           const float (&w)[NB][4], float (&o)[NB][D / 16][4]) {
+__device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* scales, int r, int t, int usable, const uint32_t (&sc)[2],
+                                           float down, const float (&w)[NB][4], float (&o)[NB][D / 16][4]) {
   int key[4];                                         // keys of contraction indices 2t, 2t + 1, 2t + 8, 2t + 9
   key[0] = t, key[1] = 4 + (t ^ 1), key[2] = 8 + t, key[3] = 12 + (t ^ 1);
   if constexpr (FMT == kFmtInt4) {
     // words 8 r' .. of each group of 64: m-tile j of a group has row r = element 8 r + 2j, row r + 8 the next
-    const int k0 = key_of_row(r), k1 = k0 + 8;
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
-      const float s0 = WHOLE || k0 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k0 * (D / 32) + 2 * g)) : 0.f;
-      const float s1 = WHOLE || k1 < usable ? __half2float(*reinterpret_cast<const __half*>(scales + k1 * (D / 32) + 2 * g)) : 0.f;
-      uint32_t bh[NB][2], bl[NB][2];
+      const float s0 = int4_scale(sc[0], g) * down, s1 = int4_scale(sc[1], g) * down;
+      uint32_t b[NB][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float s = half ? s1 : s0;
-          const float a = w[nb][2 * half] * s, b = w[nb][2 * half + 1] * s;
-          const uint32_t hi = pack_bf16x2(a, b);
-          const uint32_t lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
-          bh[nb][half] = movmatrix(hi);
-          bl[nb][half] = movmatrix(lo);
-        }
+      for (int nb = 0; nb < NB; ++nb) {
+        b[nb][0] = movmatrix(pack_f16x2(w[nb][0] * s0, w[nb][1] * s0));
+        b[nb][1] = movmatrix(pack_f16x2(w[nb][2] * s1, w[nb][3] * s1));
+      }
       uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint32_t*>(codes + key[i] * (D / 2) + 32 * g + 4 * r) ^ 0x88888888u;
+      for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint32_t*>(codes + key[i] * (D / 2) + 32 * g + 4 * r);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {          // codes 0..3, 4..7 of the words
-        const uint32_t x = __byte_perm(c[0], c[1], half ? 0x7632 : 0x5410);
-        const uint32_t y = __byte_perm(c[2], c[3], half ? 0x7632 : 0x5410);
+      for (int half = 0; half < 2; ++half) {          // codes 0..3, 4..7 of the words: (key a, key b) pairs
         uint32_t ux[4], uy[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {                 // 128 + u in bf16, minus 136
-          const uint32_t px = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u, py = ((y >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-          asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(ux[i]) : "r"(px), "r"(0x43084308u));
-          asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(uy[i]) : "r"(py), "r"(0x43084308u));
-        }
+        int4x8_to_f16(__byte_perm(c[0], c[1], half ? 0x7632 : 0x5410), ux);
+        int4x8_to_f16(__byte_perm(c[2], c[3], half ? 0x7632 : 0x5410), uy);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t a[4] = {ux[2 * j], ux[2 * j + 1], uy[2 * j], uy[2 * j + 1]};
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma_bf16_16816(o[nb][4 * g + 2 * half + j], a, bh[nb][0], bh[nb][1]);
-            mma_bf16_16816(o[nb][4 * g + 2 * half + j], a, bl[nb][0], bl[nb][1]);
-          }
+          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(o[nb][4 * g + 2 * half + j], a, b[nb][0], b[nb][1]);
         }
       }
     }
@@ -362,12 +353,42 @@ __device__ __forceinline__ int value_element(int r, int j) {
 template <int FMT, int D, int NB, bool WHOLE>
 __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int base, int have, int limit, const uint32_t (&qf)[NB][D / 8],
                                          const float (&factor)[NB][2], const int (&lo_key)[NB][2], const int (&hi_key)[NB][2],
-                                         float (&m)[NB][2], float (&l)[NB][2], float (&o)[NB][D / 16][4]) {
+                                         float (&m)[NB][2], float (&l)[NB][2], float (&o)[NB][D / 16][4], int& vexp) {
   constexpr int SB = kv_scale_bytes(FMT, D);
   const uint8_t* ks = kc + kDecChunk * (D / 2);
   const uint8_t* vc = kc + kDecChunk * (D / 2 + SB);
   const uint8_t* vs = vc + kDecChunk * (D / 2);
   const int kr = key_of_row(r);
+  // INT4: the value scales of this lane's keys, and the running power of two that they are divided by, so that
+  // the weights times scales, at most 2^14 * 2, fit fp16
+  uint32_t sv[kDecBlocks][2];
+  if constexpr (FMT == kFmtInt4) {
+    uint32_t big = 0u;
+#pragma unroll
+    for (int u = 0; u < kDecBlocks; ++u)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint8_t* at = vs + (16 * u + kr + 8 * k) * SB;
+        uint32_t two = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+        if (!WHOLE && (!((have >> u) & 1) || base + 16 * u + kr + 8 * k >= limit)) two = 0u;
+        sv[u][k] = two;
+        big = __vmaxu2(big, two);                     // fp16 of one sign order like integers
+      }
+    big = max(big & 0xffffu, big >> 16);
+    const int e = max(static_cast<int>((__float_as_uint(int4_scale(big, 0)) >> 23) & 255u) - 127, -24);
+    if (__any_sync(0xffffffffu, e > vexp)) {
+      const int e2 = max(vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, e)));
+      const float f = vexp > -100 ? __uint_as_float(static_cast<uint32_t>(vexp - e2 + 127) << 23) : 1.f;   // the sums are 0 at first
+      vexp = e2;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[nb][d][i] *= f;
+    }
+  }
+  const float down = FMT == kFmtInt4 ? __uint_as_float(static_cast<uint32_t>(127 - vexp) << 23) : 1.f;
   float s[kDecBlocks][NB][4];
 #pragma unroll
   for (int u = 0; u < kDecBlocks; ++u) {
@@ -412,7 +433,7 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float sub = m[nb][j] == -INFINITY ? 0.f : m[nb][j] - 15.f;
+      const float sub = m[nb][j] == -INFINITY ? 0.f : m[nb][j] - dec_shift(FMT);
 #pragma unroll
       for (int u = 0; u < kDecBlocks; ++u)
 #pragma unroll
@@ -425,18 +446,19 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
 #pragma unroll
   for (int u = 0; u < kDecBlocks; ++u) {
     const int usable = WHOLE ? 16 : (((have >> u) & 1) ? limit - base - 16 * u : 0);
-    add_values<FMT, D, NB, WHOLE>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, usable, s[u], o);
+    add_values<FMT, D, NB, WHOLE>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, usable, sv[u], down, s[u], o);
   }
 }
 
 // Writes four elements of a finished row, and its lse.
+template <int FMT>
 __device__ __forceinline__ void write_row(const AttnParams& p, int row0, int h, int row, int d, int D, float4 acc, float top, float sum) {
   const int i = row / p.rep, hq = h * p.rep.d + row - i * p.rep.d;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   *reinterpret_cast<uint2*>(p.out + (row0 + i) * p.out_stride + hq * D + d) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (p.lse != nullptr && d == 0)
-    p.lse[static_cast<long long>(row0 + i) * p.q_heads + hq] = sum > 0.f ? (top - 15.f + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    p.lse[static_cast<long long>(row0 + i) * p.q_heads + hq] = sum > 0.f ? (top - dec_shift(FMT) + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int FMT, int D, int NB>
@@ -513,6 +535,10 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         const int k = lane << piece_log2, off = (key0 + k) & (p.g.page - 1);
         const uint8_t* blk = p.g.pool + kv_block(p.g, page, h);
         uint8_t* dst = ring + st * STAGE;
+        if (p.g.page_log2 == 6) {                     // a page of 64 keys lies in the order of a stage
+          bulk_load(dst, blk, STAGE, &bars[st]);
+          return;
+        }
         bulk_load(dst + k * (D / 2), blk + off * (D / 2), piece * (D / 2), &bars[st]);
         bulk_load(dst + kDecChunk * (D / 2) + k * SB, blk + p.g.ks + off * SB, piece * SB, &bars[st]);
         bulk_load(dst + STAGE / 2 + k * (D / 2), blk + p.g.vc + off * (D / 2), piece * (D / 2), &bars[st]);
@@ -572,7 +598,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
     }
 
     int base = first + warp * kDecChunk;
-    int st = 0;
+    int st = 0, vexp = -1000;
     for (int left = dead ? 0 : steps; left > 0; --left) {
       const int page = page_of(next);                 // looked up a step ahead of its copy
       if (!warp_wait(&bars[st], (phase >> st) & 1, p.budget, nullptr)) {
@@ -588,9 +614,9 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
       const uint8_t* kc = ring + st * STAGE;
       const int have = loaded[st];
       if (have == (1 << kDecBlocks) - 1 && base >= all_lo && base + kDecChunk <= all_hi)
-        dec_step<FMT, D, NB, true>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o);
+        dec_step<FMT, D, NB, true>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
       else
-        dec_step<FMT, D, NB, false>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o);
+        dec_step<FMT, D, NB, false>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
       phase ^= 1u << st;
       --flying;
       __syncwarp();                                   // every lane has left the stage
@@ -625,7 +651,8 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         float top = row_max[row];
 #pragma unroll
         for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, row_max[w * RT + row]);
-        const float c = m[nb][j] == -INFINITY ? 0.f : ex2(m[nb][j] - top);
+        float c = m[nb][j] == -INFINITY ? 0.f : ex2(m[nb][j] - top);
+        if (FMT == kFmtInt4) c *= __uint_as_float(static_cast<uint32_t>(max(vexp, -24) + 127) << 23);
 #pragma unroll
         for (int d = 0; d < D / 16; ++d)
           *reinterpret_cast<float2*>(sums + row * PITCH + value_element<FMT, D>(r, d)) =
@@ -654,7 +681,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
       }
       if (!split) {
-        write_row(p, req.row0, h, rt * RT + row, d, D, acc, top, sum);
+        write_row<FMT>(p, req.row0, h, rt * RT + row, d, D, acc, top, sum);
       } else {
         __stcg(reinterpret_cast<float4*>(slot + row * D + d), acc);
         if (d == 0) __stcg(reinterpret_cast<float2*>(slot + RT * D + 2 * row), make_float2(top, sum));
@@ -688,7 +715,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
             acc.z = acc.z * f0 + v.z * f1, acc.w = acc.w * f0 + v.w * f1;
             top = m2;
           }
-          write_row(p, req.row0, h, rt * RT + row, d, D, acc, top, sum);
+          write_row<FMT>(p, req.row0, h, rt * RT + row, d, D, acc, top, sum);
         }
       }
     }
