@@ -28,7 +28,14 @@ int dec_blocks(const svdq_kv_attention_desc* d) {
   const long long rep = d->q_heads / d->cache.kv_heads;
   return d->batch > 0 && static_cast<long long>(d->rows) * rep > 8LL * d->batch ? 2 : 1;
 }
-constexpr int kDecCtasPerSm = 3;
+// One CTA of 12 warps per SM where the items (key heads of requests) are no more than the SMs: an SM then works on
+// one or two items, whose steps all its warps share.  With more items the ends of the items cost more than that
+// gives, and three CTAs of 4 warps cover for one another.
+bool dec_wide(const svdq_kv_attention_desc* d, int nb, int sms) {
+  const long long rep = d->q_heads / d->cache.kv_heads;
+  const long long tiles = std::min<long long>(d->rows, (static_cast<long long>(d->rows) * rep + 8 * nb - 1) / (8 * nb) + d->batch);
+  return tiles * d->cache.kv_heads <= sms;
+}
 
 // The tcgen05 kernel takes the call where a key head has more than this many query rows per request.
 constexpr int kRowsFrom = 32;
@@ -38,13 +45,18 @@ bool many_rows(const svdq_kv_attention_desc* d) {
 
 using AttnKernel = void (*)(AttnParams);
 
-template <int FMT>
-AttnKernel dec_kernel_of(int D, int nb) {
-  if (D == 64) return nb == 1 ? kv_attn_decode_kernel<FMT, 64, 1> : kv_attn_decode_kernel<FMT, 64, 2>;
-  return nb == 1 ? kv_attn_decode_kernel<FMT, 128, 1> : kv_attn_decode_kernel<FMT, 128, 2>;
+template <int FMT, int D, int NB>
+AttnKernel dec_kernel_for(bool wide) {
+  return wide ? kv_attn_decode_kernel<FMT, D, NB, kDecWide> : kv_attn_decode_kernel<FMT, D, NB, kDecNarrow>;
 }
-AttnKernel dec_kernel(int fmt, int D, int nb) {
-  return fmt == SVDQ_NVFP4 ? dec_kernel_of<kFmtNvfp4>(D, nb) : fmt == SVDQ_INT4 ? dec_kernel_of<kFmtInt4>(D, nb) : dec_kernel_of<kFmtFp4g32>(D, nb);
+template <int FMT>
+AttnKernel dec_kernel_of(int D, int nb, bool wide) {
+  if (D == 64) return nb == 1 ? dec_kernel_for<FMT, 64, 1>(wide) : dec_kernel_for<FMT, 64, 2>(wide);
+  return nb == 1 ? dec_kernel_for<FMT, 128, 1>(wide) : dec_kernel_for<FMT, 128, 2>(wide);
+}
+AttnKernel dec_kernel(int fmt, int D, int nb, bool wide) {
+  return fmt == SVDQ_NVFP4 ? dec_kernel_of<kFmtNvfp4>(D, nb, wide)
+         : fmt == SVDQ_INT4 ? dec_kernel_of<kFmtInt4>(D, nb, wide) : dec_kernel_of<kFmtFp4g32>(D, nb, wide);
 }
 
 template <int FMT>
@@ -82,8 +94,9 @@ int kv_device(int* dev) {
   for (int fmt : {SVDQ_NVFP4, SVDQ_INT4, SVDQ_FP4G32})
     for (int D : {64, 128})
       for (int nb : {1, 2})
-        SVDQ_CUDA(cudaFuncSetAttribute(dec_kernel(fmt, D, nb), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(dec_smem_bytes(fmt, D, nb))));
+        for (int wide : {0, 1})
+          SVDQ_CUDA(cudaFuncSetAttribute(dec_kernel(fmt, D, nb, wide), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(dec_smem_bytes(fmt, D, nb, wide ? kDecWide : kDecNarrow))));
   for (int fmt : {SVDQ_NVFP4, SVDQ_INT4, SVDQ_FP4G32})
     for (int D : {64, 128}) {
       int smem = 0;
@@ -353,12 +366,15 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
     return SVDQ_OK;
   }
   const int nb = dec_blocks(d);
+  const bool wide = dec_wide(d, nb, g_dev[dev].sms);
+  const int warps = wide ? kDecWide : kDecNarrow, unit = warps * kDecChunk;
   // enough CTAs for the most units that these rows and this table can hold
   const long long tiles = std::min<long long>((static_cast<long long>(d->rows) * p.rep.d + 8 * nb - 1) / (8 * nb) + d->batch,
                                               static_cast<long long>(d->rows) * p.rep.d);
-  const long long units = tiles * p.g.heads * std::max<long long>(1, ((static_cast<long long>(p.width) << p.g.page_log2) + kDecUnit - 1) / kDecUnit + 1);
-  const int ctas = static_cast<int>(std::min<long long>(units, static_cast<long long>(g_dev[dev].sms) * kDecCtasPerSm));
-  SVDQ_CUDA(launch_pdl(dec_kernel(d->cache.fmt, p.g.D, nb), dim3(ctas), dim3(kDecThreads), dec_smem_bytes(d->cache.fmt, p.g.D, nb), st, 0u, p));
+  const long long units = tiles * p.g.heads * std::max<long long>(1, ((static_cast<long long>(p.width) << p.g.page_log2) + unit - 1) / unit + 1);
+  const int ctas = static_cast<int>(std::min<long long>(units, static_cast<long long>(g_dev[dev].sms) * (wide ? 1 : 3)));
+  SVDQ_CUDA(launch_pdl(dec_kernel(d->cache.fmt, p.g.D, nb, wide), dim3(ctas), dim3(32 * warps), dec_smem_bytes(d->cache.fmt, p.g.D, nb, warps), st,
+                       0u, p));
   return SVDQ_OK;
 }
 

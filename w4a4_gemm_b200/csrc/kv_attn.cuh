@@ -41,21 +41,20 @@
 
 namespace svdq {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecChunk = 64;                       // keys of a warp's step
 constexpr int kDecBlocks = kDecChunk / 16;
-constexpr int kDecUnit = kDecChunk * kDecWarps;     // keys of a unit of work
 constexpr int kDecStages = 2;
+// CTAs of 4 warps, three to an SM, or one CTA of 12 (see kv_api.cuh).  A unit of work is a step of every warp.
+constexpr int kDecWide = 12, kDecNarrow = 4;
 // The weights are exp2(x - max + shift).
 __host__ __device__ constexpr float dec_shift(int fmt) { return fmt == kFmtInt4 ? 14.f : 15.f; }
 
 __host__ __device__ constexpr int dec_stage_bytes(int fmt, int D) {
   return 2 * kDecChunk * (D / 2 + kv_scale_bytes(fmt, D));
 }
-__host__ __device__ constexpr uint32_t dec_smem_bytes(int fmt, int D, int NB) {
-  return static_cast<uint32_t>(kDecWarps * kDecStages * dec_stage_bytes(fmt, D) + kDecWarps * kDecStages * 8 /* barriers */ +
-                               kDecWarps * kDecStages * 4 /* blocks */ + 2 * kDecWarps * 8 * NB * 4 /* max, sum */ + 128);
+__host__ __device__ constexpr uint32_t dec_smem_bytes(int fmt, int D, int NB, int warps) {
+  return static_cast<uint32_t>(warps * kDecStages * (dec_stage_bytes(fmt, D) + 8 /* barriers */ + 8 /* what was loaded */) +
+                               2 * warps * 8 * NB * 4 /* max, sum */ + 128);
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -105,12 +104,24 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// (a & b) ^ c and the bits of a where m is set, of b elsewhere, in one instruction each.
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t bit_select(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(d) : "r"(a), "r"(b), "r"(m));
+  return d;
+}
+
 // Four 4-bit two's complement codes of each half word -> four fp16 pairs, pair i from bits 4i of both halves: u =
 // code ^ 8 under the exponent of 1024 is 1024 + u (or 1024 + 16 u), minus 1032 (or / 16, minus 72).
 __device__ __forceinline__ void int4x8_to_f16(uint32_t x, uint32_t* h) {
   const uint32_t y = x >> 8;
-  const uint32_t p[4] = {(x & 0x000F000Fu) ^ 0x64086408u, (x & 0x00F000F0u) ^ 0x64806480u, (y & 0x000F000Fu) ^ 0x64086408u,
-                         (y & 0x00F000F0u) ^ 0x64806480u};
+  const uint32_t p[4] = {and_xor(x, 0x000F000Fu, 0x64086408u), and_xor(x, 0x00F000F0u, 0x64806480u), and_xor(y, 0x000F000Fu, 0x64086408u),
+                         and_xor(y, 0x00F000F0u, 0x64806480u)};
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(p[i]), "r"(0x64086408u));                               // 1032
@@ -324,8 +335,8 @@ __device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* 
     for (int v = 0; v < W; ++v) {
       // bytes (key a's code, key b's code) of the even and the odd elements
       const uint32_t m = 0x0F0F0F0Fu;
-      const uint32_t e01 = (c[0][v] & m) | ((c[1][v] << 4) & ~m), o01 = ((c[0][v] >> 4) & m) | (c[1][v] & ~m);
-      const uint32_t e23 = (c[2][v] & m) | ((c[3][v] << 4) & ~m), o23 = ((c[2][v] >> 4) & m) | (c[3][v] & ~m);
+      const uint32_t e01 = bit_select(c[0][v], c[1][v] << 4, m), o01 = bit_select(c[0][v] >> 4, c[1][v], m);
+      const uint32_t e23 = bit_select(c[2][v], c[3][v] << 4, m), o23 = bit_select(c[2][v] >> 4, c[3][v], m);
       uint32_t f[4][4];
       e2m1x8_to_f16(e01, f[0]);
       e2m1x8_to_f16(o01, f[1]);
@@ -461,9 +472,10 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int row0, int h, 
     p.lse[static_cast<long long>(row0 + i) * p.q_heads + hq] = sum > 0.f ? (top - dec_shift(FMT) + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int FMT, int D, int NB>
-__global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const AttnParams p) {
+template <int FMT, int D, int NB, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn_decode_kernel(const AttnParams p) {
   constexpr int RT = 8 * NB;
+  constexpr int UNIT = kDecChunk * WARPS;
   constexpr int STAGE = dec_stage_bytes(FMT, D);
   constexpr int SB = kv_scale_bytes(FMT, D);
   constexpr int PITCH = D + 4;                        // floats of a row of the joined sums
@@ -471,20 +483,22 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int warp = static_cast<int>(warp_id()), lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
   uint8_t* ring = dec_smem + warp * kDecStages * STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(dec_smem + kDecWarps * kDecStages * STAGE) + warp * kDecStages;
-  int* loaded = reinterpret_cast<int*>(dec_smem + kDecWarps * kDecStages * (STAGE + 8)) + warp * kDecStages;
-  float* row_max = reinterpret_cast<float*>(dec_smem + kDecWarps * kDecStages * (STAGE + 12));   // [warps][RT]
-  float* row_sum = row_max + kDecWarps * RT;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(dec_smem + WARPS * kDecStages * STAGE) + warp * kDecStages;
+  int2* loaded = reinterpret_cast<int2*>(dec_smem + WARPS * kDecStages * (STAGE + 8)) + warp * kDecStages;   // blocks, first key
+  float* row_max = reinterpret_cast<float*>(dec_smem + WARPS * kDecStages * (STAGE + 16));   // [warps][RT]
+  float* row_sum = row_max + WARPS * RT;
   __shared__ Share share;
   __shared__ int last_flag;
+  __shared__ int claims[2];                           // steps of the segment that warps have taken; two segments in turn
 
   griddep_launch_dependents();
+  if (threadIdx.x < 2) claims[threadIdx.x] = 0;
   if (lane == 0) {
     for (int s = 0; s < kDecStages; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
   griddep_wait();
-  find_share<RT, kDecUnit>(p, reinterpret_cast<long long*>(dec_smem), &share);
+  find_share<RT, UNIT>(p, reinterpret_cast<long long*>(dec_smem), &share);
   fence_proxy_async_smem();                           // the scan's words lie under the rings
   int count = share.count;
   if (count == 0) return;
@@ -493,6 +507,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
   Request req = load_request(p, b);
   uint32_t phase = 0;                                 // bit s: parity of stage s
   bool dead = false;                                  // a wait ran out
+  uint32_t seg = 0;
 
   // Pieces of a step that lie in one page are copied by lanes 0 .. pieces - 1.
   const int piece_log2 = min(p.g.page_log2, 6);
@@ -502,20 +517,26 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
 
   while (true) {
     int k0, k1;
-    tile_keys<RT, kDecUnit>(p, req, rt, k0, k1);
-    const int units = max(1, (k1 - k0 + kDecUnit - 1) / kDecUnit);
+    tile_keys<RT, UNIT>(p, req, rt, k0, k1);
+    const int units = max(1, (k1 - k0 + UNIT - 1) / UNIT);
     const int here = min(units - unit, count);
-    const int first = k0 + unit * kDecUnit;           // keys of this segment
-    const int limit = here >= units - unit ? k1 : first + here * kDecUnit;
+    const int first = k0 + unit * UNIT;           // keys of this segment
+    const int limit = here >= units - unit ? k1 : first + here * UNIT;
     const int* table = p.table + b * p.table_stride;
-    int next = first + warp * kDecChunk;              // first key of the next step to be copied; kDecUnit apart
-    const int steps = limit > next ? (limit - next + kDecUnit - 1) / kDecUnit : 0;
+    // Steps go to whichever warp is next: the scheduler serves older warps first, and equal shares would leave the
+    // others alone at the end.
+    auto claim = [&]() {
+      int c = 0;
+      if (lane == 0) c = atomicAdd(&claims[seg & 1], 1);
+      const long long key = first + static_cast<long long>(__shfl_sync(0xffffffffu, c, 0)) * kDecChunk;
+      return key < limit ? static_cast<int>(key) : -1;      // first key of the step, or none left
+    };
 
     // The page of this lane's piece of the step at `next`: -1 past the end, or outside the pool.
     auto page_of = [&](int key0) {
       const int key = key0 + (lane << piece_log2);
       int page = -1;
-      if (copier && key < limit) {
+      if (copier && key0 >= 0 && key < limit) {
         page = table[key >> p.g.page_log2];
         if (page >= p.g.num_pages) page = -2;
         if (page < 0) raise_error(kErrIndex);
@@ -527,7 +548,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
       if (lane == 0) {
         // a bit per piece becomes a bit per 16 keys
         const unsigned spread = piece_log2 == 4 ? good : piece_log2 == 5 ? (good & 1) * 3 + (good >> 1) * 12 : good * 15;
-        loaded[st] = static_cast<int>(spread);
+        loaded[st] = make_int2(static_cast<int>(spread), key0);
         mbar_arrive_expect_tx(&bars[st], (__popc(good) << piece_log2) * 2 * (D / 2 + SB));
       }
       __syncwarp();
@@ -545,18 +566,22 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         bulk_load(dst + STAGE / 2 + kDecChunk * (D / 2) + k * SB, blk + p.g.vs + off * SB, piece * SB, &bars[st]);
       }
     };
-    int flying = 0;                                   // copies on their way
+    int flying = 0;                                   // stages filled or on their way
+    int next = -1;                                    // the step after those
     if (!dead) {
-      int pages[kDecStages];
+      int keys[kDecStages], pages[kDecStages];
 #pragma unroll
-      for (int s = 0; s < kDecStages; ++s) pages[s] = page_of(next + s * kDecUnit);
+      for (int s = 0; s < kDecStages; ++s) {
+        keys[s] = s == 0 || keys[s ? s - 1 : 0] >= 0 ? claim() : -1;
+        pages[s] = page_of(keys[s]);
+      }
 #pragma unroll
       for (int s = 0; s < kDecStages; ++s)
-        if (s < steps) {
-          issue(s, next, pages[s]);
-          next += kDecUnit;
+        if (keys[s] >= 0) {
+          issue(s, keys[s], pages[s]);
           ++flying;
         }
+      if (flying == kDecStages) next = claim();
     }
 
     // this lane's score columns: rows 2t, 2t + 1 of each block
@@ -597,9 +622,8 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         for (int i = 0; i < 4; ++i) o[nb][d][i] = 0.f;
     }
 
-    int base = first + warp * kDecChunk;
     int st = 0, vexp = -1000;
-    for (int left = dead ? 0 : steps; left > 0; --left) {
+    while (flying > 0) {
       const int page = page_of(next);                 // looked up a step ahead of its copy
       if (!warp_wait(&bars[st], (phase >> st) & 1, p.budget, nullptr)) {
         if (lane == 0) raise_error(kErrWaitAttn);
@@ -612,7 +636,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         break;
       }
       const uint8_t* kc = ring + st * STAGE;
-      const int have = loaded[st];
+      const int have = loaded[st].x, base = loaded[st].y;
       if (have == (1 << kDecBlocks) - 1 && base >= all_lo && base + kDecChunk <= all_hi)
         dec_step<FMT, D, NB, true>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
       else
@@ -620,12 +644,11 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
       phase ^= 1u << st;
       --flying;
       __syncwarp();                                   // every lane has left the stage
-      if (left > kDecStages) {
+      if (next >= 0) {
         issue(st, next, page);
-        next += kDecUnit;
         ++flying;
+        next = claim();
       }
-      base += kDecUnit;
       st = st + 1 == kDecStages ? 0 : st + 1;
     }
 
@@ -650,7 +673,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
         const int row = nb * 8 + 2 * t + j;
         float top = row_max[row];
 #pragma unroll
-        for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, row_max[w * RT + row]);
+        for (int w = 1; w < WARPS; ++w) top = fmaxf(top, row_max[w * RT + row]);
         float c = m[nb][j] == -INFINITY ? 0.f : ex2(m[nb][j] - top);
         if (FMT == kFmtInt4) c *= __uint_as_float(static_cast<uint32_t>(max(vexp, -24) + 127) << 23);
 #pragma unroll
@@ -666,15 +689,15 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
     const float* all = reinterpret_cast<const float*>(dec_smem);
     constexpr int kWarpFloats = kDecStages * STAGE / 4;
     float* slot = p.partials + (2ll * blockIdx.x + (at == share.begin ? 0 : 1)) * SLOT;
-    for (int e = threadIdx.x; e < live_rows * Q; e += kDecThreads) {
+    for (int e = threadIdx.x; e < live_rows * Q; e += (32 * WARPS)) {
       const int row = e / Q, d = e % Q * 4;
       float top = row_max[row];
 #pragma unroll
-      for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, row_max[w * RT + row]);
+      for (int w = 1; w < WARPS; ++w) top = fmaxf(top, row_max[w * RT + row]);
       float sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         const float mw = row_max[w * RT + row];
         sum += mw == -INFINITY ? 0.f : row_sum[w * RT + row] * ex2(mw - top);
         const float4 v = *reinterpret_cast<const float4*>(all + w * kWarpFloats + row * PITCH + d);
@@ -699,7 +722,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
       __syncthreads();
       if (last_flag) {
         const float* part0 = p.partials + (share_begin(share.base, share.rem, c0) == item ? 2ll * c0 : 2ll * c0 + 1) * SLOT;
-        for (int e = threadIdx.x; e < live_rows * Q; e += kDecThreads) {
+        for (int e = threadIdx.x; e < live_rows * Q; e += (32 * WARPS)) {
           const int row = e / Q, d = e % Q * 4;
           float top = -INFINITY, sum = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -721,6 +744,8 @@ __global__ void __launch_bounds__(kDecThreads, 3) kv_attn_decode_kernel(const At
     }
 
     // ------------------------------------------------ the next item of the share
+    if (threadIdx.x == 0) claims[seg & 1] = 0;        // every warp is past its last claim of this segment
+    ++seg;
     count -= here;
     at += here;
     if (count <= 0) break;
