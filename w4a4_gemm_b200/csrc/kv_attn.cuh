@@ -137,9 +137,10 @@ __device__ __forceinline__ int key_of_row(int m) {
 }
 
 // Queries of one 8-row block as B fragments of K q^T.  Lane (r, t) holds elements of row r; pair k of
-// register kk matches the key fragments below.  `f` receives 2^e of the row.
+// register kk matches the key fragments below.  `f` receives 2^e of the row; `negate`: for a
+// negative scale, which turns the queries round.
 template <int FMT, int D>
-__device__ __forceinline__ void load_queries(const __nv_bfloat16* row, bool live, int t, uint32_t (&qf)[D / 8], float& f) {
+__device__ __forceinline__ void load_queries(const __nv_bfloat16* row, bool live, int t, bool negate, uint32_t (&qf)[D / 8], float& f) {
   constexpr int N = D / 4;                            // elements of this lane
   float v[N];
 #pragma unroll
@@ -166,7 +167,7 @@ __device__ __forceinline__ void load_queries(const __nv_bfloat16* row, bool live
   // 2^e with 2^12 <= amax / 2^e < 2^13; both factors stay normal
   const int e = min(max(static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 127 - 12, -120), 120);
   f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  const float inv = __uint_as_float((static_cast<uint32_t>(127 - e) << 23) | (negate ? 0x80000000u : 0u));
 #pragma unroll
   for (int i = 0; i < N; i += 8) {
 #pragma unroll
@@ -408,7 +409,6 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[u][nb][i] *= factor[nb][i & 1];
         if (!WHOLE) {
           const int key = base + 16 * u + kr + (i & 2 ? 8 : 0);
           const bool see = ((have >> u) & 1) && key < limit && key < hi_key[nb][i & 1] && key >= lo_key[nb][i & 1];
@@ -418,12 +418,13 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
   }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    float top[2];
+    float top[2];                                       // the factors are positive
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       top[j] = fmaxf(s[0][nb][j], s[0][nb][j + 2]);
 #pragma unroll
       for (int u = 1; u < kDecBlocks; ++u) top[j] = fmax3(top[j], s[u][nb][j], s[u][nb][j + 2]);
+      top[j] *= factor[nb][j];
     }
     // a lane whose own maximum passes the running one makes the warp look for the new one
     if (__any_sync(0xffffffffu, top[0] > m[nb][0] || top[1] > m[nb][1])) {
@@ -442,17 +443,20 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[nb][d][i] *= c2[i & 1];
     }
+    const float2 f2 = make_float2(factor[nb][0], factor[nb][1]);
+    const float2 b2 = make_float2(m[nb][0] == -INFINITY ? 0.f : dec_shift(FMT) - m[nb][0], m[nb][1] == -INFINITY ? 0.f : dec_shift(FMT) - m[nb][1]);
+    float2 sum = make_float2(l[nb][0], l[nb][1]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float sub = m[nb][j] == -INFINITY ? 0.f : m[nb][j] - dec_shift(FMT);
+    for (int u = 0; u < kDecBlocks; ++u)
 #pragma unroll
-      for (int u = 0; u < kDecBlocks; ++u)
-#pragma unroll
-        for (int i = j; i < 4; i += 2) {
-          s[u][nb][i] = ex2(s[u][nb][i] - sub);
-          l[nb][j] += s[u][nb][i];
-        }
-    }
+      for (int i = 0; i < 4; i += 2) {
+        const float2 x = ffma2(make_float2(s[u][nb][i], s[u][nb][i + 1]), f2, b2);
+        s[u][nb][i] = ex2(x.x);
+        s[u][nb][i + 1] = ex2(x.y);
+        sum = fadd2(sum, make_float2(s[u][nb][i], s[u][nb][i + 1]));
+      }
+    l[nb][0] = sum.x;
+    l[nb][1] = sum.y;
   }
 #pragma unroll
   for (int u = 0; u < kDecBlocks; ++u) {
@@ -595,10 +599,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
       const bool live = row < rows;
       const int i = live ? row / p.rep : 0, hq = h * p.rep.d + (live ? row - i * p.rep.d : 0);
       float f;
-      load_queries<FMT, D>(p.q + (req.row0 + i) * p.q_stride + hq * D, live, t, qf[nb], f);
+      load_queries<FMT, D>(p.q + (req.row0 + i) * p.q_stride + hq * D, live, t, p.scale < 0.f, qf[nb], f);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        factor[nb][j] = __shfl_sync(0xffffffffu, f, (2 * t + j) * 4) * (p.scale * 1.4426950408889634f);
+        factor[nb][j] = fmaxf(__shfl_sync(0xffffffffu, f, (2 * t + j) * 4) * (fabsf(p.scale) * 1.4426950408889634f), 1.17549435e-38f);
         const int pos = req.kv - req.n + min(rt * RT + nb * 8 + 2 * t + j, rows - 1) / p.rep;
         hi_key[nb][j] = p.causal ? min(req.kv, pos + 1) : req.kv;
         lo_key[nb][j] = p.window > 0 ? pos - p.window + 1 : 0;
