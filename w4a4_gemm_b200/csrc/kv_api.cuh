@@ -133,6 +133,26 @@ int kv_geometry(const svdq_kv_cache* c, KvGeom* g, bool need_pool) {
   return SVDQ_OK;
 }
 
+// The grid of append or read, `values` to a piece, and the rows of a thread: several where there are enough pieces for
+// every thread that the SMs hold, so that more loads are in flight; one where latency counts.
+int append_grid(int M, const KvGeom& g, int values, int sms, dim3* grid) {
+  const int per_row = 2 * g.heads * (g.D / values);
+  const int units = static_cast<long long>(M) * per_row >= static_cast<long long>(sms) * 2048 * kAppendUnits ? kAppendUnits : 1;
+  const int rows = units * std::max(1, kAppendThreads / per_row);      // of a CTA
+  *grid = dim3((M + rows - 1) / rows, std::max(1, (per_row + kAppendThreads - 1) / kAppendThreads));
+  return units;
+}
+
+template <typename Out>
+using ReadKernel = void (*)(KvGeom, const long long*, int, Out*, Out*);
+
+template <typename Out>
+ReadKernel<Out> read_kernel(int fmt, bool many) {
+  if (fmt == SVDQ_NVFP4) return many ? kv_read_kernel<0, Out, kAppendUnits> : kv_read_kernel<0, Out, 1>;
+  if (fmt == SVDQ_INT4) return many ? kv_read_kernel<1, Out, kAppendUnits> : kv_read_kernel<1, Out, 1>;
+  return many ? kv_read_kernel<2, Out, kAppendUnits> : kv_read_kernel<2, Out, 1>;
+}
+
 using NormKernel = void (*)(NormRopeParams);
 
 template <int LANES>
@@ -242,10 +262,11 @@ SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* d, void* stream) {
   p.eps = d->eps;
   const int lanes_log2 = log2_exact((d->head_dim + 7) / 8);   // of a head
   const int heads = d->q_heads + d->k_heads;
-  // Heads that a lane group walks: as many as leave two waves of resident warps (64 per SM), at most 16; each row's
-  // cosines and sines are then loaded once per chunk.  Few rows take a head per group: latency counts there.
+  // Heads that a lane group walks: as many as leave two waves of the 512 threads that an SM holds, at most 16; each
+  // row's cosines and sines are then loaded once per chunk (4608 x 48 heads: 21.6 us, with chunks of 8 24 us).  Few
+  // rows take a head per group: latency counts there.
   const long long lanes = static_cast<long long>(d->rows) << lanes_log2;
-  const long long want = static_cast<long long>(g_dev[dev].sms) * 2048 * 2;
+  const long long want = static_cast<long long>(g_dev[dev].sms) * 512 * 2;
   p.chunk = static_cast<int>(std::max<long long>(1, std::min<long long>(16, lanes * heads / want)));
   if (p.chunk >= kNormBatch) p.chunk = p.chunk / kNormBatch * kNormBatch;
   p.chunks = (heads + p.chunk - 1) / p.chunk;
@@ -266,16 +287,13 @@ SVDQ_API int svdq_kv_append(const svdq_kv_cache* cache, const void* k, const voi
   if (slots == nullptr || !rows_ok(k, k_stride) || !rows_ok(v, v_stride)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
-  const long long threads = static_cast<long long>(M) * 2 * g.heads * (g.D / 16);
-  const long long ctas = (threads + kAppendThreads - 1) / kAppendThreads;
-  if (ctas > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid(static_cast<unsigned>(ctas)), blk(kAppendThreads);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(k);
-  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(v);
-  const long long* sl = reinterpret_cast<const long long*>(slots);
-  auto* kernel = cache->fmt == SVDQ_NVFP4 ? kv_append_kernel<0> : cache->fmt == SVDQ_INT4 ? kv_append_kernel<1> : kv_append_kernel<2>;
-  SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, g, kp, vp, k_stride, v_stride, sl, M));
+  dim3 grid;
+  const bool many = append_grid(M, g, 8, g_dev[dev].sms, &grid) > 1;
+  auto* kernel = cache->fmt == SVDQ_NVFP4 ? (many ? kv_append_kernel<0, kAppendUnits> : kv_append_kernel<0, 1>)
+                 : cache->fmt == SVDQ_INT4 ? (many ? kv_append_kernel<1, kAppendUnits> : kv_append_kernel<1, 1>)
+                                           : (many ? kv_append_kernel<2, kAppendUnits> : kv_append_kernel<2, 1>);
+  SVDQ_CUDA(launch_pdl(kernel, grid, dim3(kAppendThreads), 0, static_cast<cudaStream_t>(stream), 0u, g, static_cast<const __nv_bfloat16*>(k),
+                       static_cast<const __nv_bfloat16*>(v), k_stride, v_stride, reinterpret_cast<const long long*>(slots), M));
   return SVDQ_OK;
 }
 
@@ -289,19 +307,16 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
   if (slots == nullptr || k == nullptr || v == nullptr || !aligned16(k) || !aligned16(v)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
-  const long long threads = static_cast<long long>(M) * 2 * g.heads * (g.D / 16);
-  const long long ctas = (threads + kAppendThreads - 1) / kAppendThreads;
-  if (ctas > 0x7fffffffLL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid(static_cast<unsigned>(ctas)), blk(kAppendThreads);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  dim3 grid;
+  const bool many = append_grid(M, g, out_fp32 ? 4 : 8, g_dev[dev].sms, &grid) > 1;
   const long long* sl = reinterpret_cast<const long long*>(slots);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (out_fp32) {
-    auto* kernel = cache->fmt == SVDQ_NVFP4 ? kv_read_kernel<0, float> : cache->fmt == SVDQ_INT4 ? kv_read_kernel<1, float> : kv_read_kernel<2, float>;
-    SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, g, sl, M, static_cast<float*>(k), static_cast<float*>(v)));
+    SVDQ_CUDA(launch_pdl(read_kernel<float>(cache->fmt, many), grid, dim3(kAppendThreads), 0, st, 0u, g, sl, M, static_cast<float*>(k),
+                         static_cast<float*>(v)));
   } else {
-    auto* kernel = cache->fmt == SVDQ_NVFP4 ? kv_read_kernel<0, __nv_bfloat16>
-                   : cache->fmt == SVDQ_INT4 ? kv_read_kernel<1, __nv_bfloat16> : kv_read_kernel<2, __nv_bfloat16>;
-    SVDQ_CUDA(launch_pdl(kernel, grid, blk, 0, st, 0u, g, sl, M, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v)));
+    SVDQ_CUDA(launch_pdl(read_kernel<__nv_bfloat16>(cache->fmt, many), grid, dim3(kAppendThreads), 0, st, 0u, g, sl, M,
+                         static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v)));
   }
   return SVDQ_OK;
 }

@@ -42,150 +42,182 @@ __device__ __forceinline__ size_t kv_block(const KvGeom& g, long long page, int 
   return (static_cast<size_t>(page) * g.heads + head) * static_cast<size_t>(g.head_bytes);
 }
 
-// 16 bf16 (two 16-byte words) -> fp32
-__device__ __forceinline__ void bf16x16_to_f32(const uint4& a, const uint4& b, float* v) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// 8 bf16 (a 16-byte word) -> fp32
+__device__ __forceinline__ void bf16x8_to_floats(const uint4& a, float* v) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     v[2 * i] = bf16_lo(w[i]);
     v[2 * i + 1] = bf16_hi(w[i]);
   }
 }
 
 // ------------------------------------------------------------------ append ---
-// One thread quantizes 16 values (32 bytes of one head's row, 8 code bytes); a
-// group of 32 or 64 meets its maximum over 2 or 4 neighbouring lanes.  The
-// quantizer is the activation kernel's, decision for decision:
+// A thread quantizes pieces of 8 values (16 bytes of one head's row, 4 code
+// bytes), so that a warp's loads and stores are whole lines; the 16, 32 or 64 values
+// of a scale meet their maximum over 2, 4 or 8 neighbouring lanes.  The quantizer is
+// the activation kernel's, decision for decision:
 // scale = rounded amax / q_max, code = round(v * RN(1 / scale)).
 // Bound by HBM at many rows (2 D bytes in, D / 2 + scales out, per head and
 // side) and by the launch at few.  A slot below 0 is a padded row and is
 // skipped; one at or past the pool's end is skipped and raises kErrIndex.
+// UNITS pieces per thread, a CTA's threads apart: their loads are issued together.
 constexpr int kAppendThreads = 256;
+constexpr int kAppendUnits = 4;
 
-template <int FMT>
+// A row has 2 heads D / VALUES pieces (keys, then values).  A thread has the same piece in UNITS rows, `step` rows
+// apart: a CTA covers 256 pieces of a row (blockIdx.y says which), or several whole rows where a row has fewer, and
+// only the slot differs from one unit to the next.
+struct Piece {
+  int row, step;                 // first row, and the rows between units; row < 0: none
+  int side, head, part;          // 0 keys, 1 values; the head; which piece of its values
+};
+template <int VALUES, int UNITS>
+__device__ __forceinline__ Piece piece_of_thread(const KvGeom& g) {
+  const int per_head = g.D / VALUES, per_row = 2 * g.heads * per_head;
+  Piece p;
+  int at = threadIdx.x, sub = 0;
+  p.step = 1;
+  if (per_row < kAppendThreads) {
+    p.step = kAppendThreads / per_row;
+    sub = at / per_row;
+    at -= sub * per_row;
+  } else {
+    at += blockIdx.y * kAppendThreads;
+  }
+  p.row = sub < p.step && at < per_row ? static_cast<int>(blockIdx.x) * p.step * UNITS + sub : -1;
+  const int head2 = at / per_head;
+  p.part = at - head2 * per_head;
+  p.side = head2 >= g.heads;
+  p.head = p.side ? head2 - g.heads : head2;
+  return p;
+}
+
+template <int FMT, int UNITS>
 __global__ void __launch_bounds__(kAppendThreads)
     kv_append_kernel(const KvGeom g, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                      long long k_stride, long long v_stride, const long long* __restrict__ slots, int M) {
   griddep_launch_dependents();
   griddep_wait();
-  const int per_head = g.D / 16;                       // threads of one head's row: 4 or 8
-  const long long n = static_cast<long long>(M) * 2 * g.heads * per_head;
-  const long long idx = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
-  // n is a multiple of 4 or 8 threads, so the lanes that share a group leave together
-  const bool live = idx < n;
-  const int part = static_cast<int>(idx % per_head);
-  const long long hr = idx / per_head;
-  const int head2 = static_cast<int>(hr % (2 * g.heads));
-  const long long row = hr / (2 * g.heads);
-  const int side = head2 >= g.heads;                   // 0 keys, 1 values
-  const int head = side ? head2 - g.heads : head2;
-  const long long slot = live ? slots[row] : -1;
-  const bool past = slot >= g.num_pages * g.page;
-  const bool ok = slot >= 0 && !past;
-  if (past && part == 0 && head2 == 0) raise_error(kErrIndex);
-  float x[16];
-  if (ok) {
-    const __nv_bfloat16* src = (side ? v + row * v_stride : k + row * k_stride) + head * g.D + part * 16;
-    const uint4* s4 = reinterpret_cast<const uint4*>(src);
-    bf16x16_to_f32(__ldg(s4), __ldg(s4 + 1), x);
-  } else {
+  const Piece pc = piece_of_thread<8, UNITS>(g);
+  // the lanes that share a group have their rows in common: they are in or out together
+  const __nv_bfloat16* src = (pc.side ? v : k) + pc.head * g.D + pc.part * 8;
+  const long long stride = pc.side ? v_stride : k_stride;
+  uint4 raw[UNITS];
+  long long slot[UNITS];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  }
-  float amax = absmax16(x);
-  constexpr int kLanes = kv_group(FMT) / 16;           // lanes that share a scale
-#pragma unroll
-  for (int o = 1; o < kLanes; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (!ok) return;
-  uint32_t codes[2] = {0u, 0u};
-  uint32_t scale;
-  if (FMT == kFmtInt4) {
-    scale = int4_scale_bits(amax);
-    const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale)));
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) codes[i / 8] |= (static_cast<uint32_t>(int4_code(x[i], inv)) & 15u) << (4 * (i % 8));
-  } else {
-    scale = e4m3_code(div6_rn(amax));
-    if (scale != 0u) {
-      const float inv = __frcp_rn(e4m3_value(scale));
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], inv);
-      codes[0] = e2m1_pack8(x);
-      codes[1] = e2m1_pack8(x + 8);
+  for (int u = 0; u < UNITS; ++u) {
+    const int row = pc.row + u * pc.step;
+    slot[u] = -1;
+    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (pc.row >= 0 && row < M) {
+      raw[u] = __ldg(reinterpret_cast<const uint4*>(src + row * stride));
+      slot[u] = slots[row];
     }
   }
-  const long long page = slot >> g.page_log2;
-  const int off = static_cast<int>(slot & (g.page - 1));
-  uint8_t* blk = g.pool + kv_block(g, page, head) + (side ? g.vc : 0);
-  *reinterpret_cast<uint2*>(blk + off * (g.D / 2) + part * 8) = make_uint2(codes[0], codes[1]);
-  uint8_t* sc = blk + g.ks + off * kv_scale_bytes(FMT, g.D);
-  if (part % kLanes == 0) {
-    if (FMT == kFmtInt4)
-      *reinterpret_cast<uint16_t*>(sc + part / kLanes * 2) = static_cast<uint16_t>(scale);
-    else
-      sc[part / kLanes] = static_cast<uint8_t>(scale);
+  const size_t page_bytes = static_cast<size_t>(g.heads) * g.head_bytes;
+  uint8_t* base = g.pool + static_cast<size_t>(pc.head) * g.head_bytes + (pc.side ? g.vc : 0);
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const bool past = slot[u] >= g.num_pages * g.page;
+    if (past && pc.part == 0 && pc.head == 0) raise_error(kErrIndex);
+    float x[8];
+    bf16x8_to_floats(raw[u], x);
+    float amax = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
+    amax = fmaxf(amax, 0.f);
+    constexpr int kLanes = kv_group(FMT) / 8;          // lanes that share a scale
+#pragma unroll
+    for (int o = 1; o < kLanes; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    uint32_t codes = 0u;
+    uint32_t scale;
+    if (FMT == kFmtInt4) {
+      scale = int4_scale_bits(amax);
+      const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(scale)));
+      const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) codes |= (static_cast<uint32_t>(int4_code(x[i], inv)) & 15u) << (4 * i);
+    } else {
+      scale = e4m3_code(div6_rn(amax));
+      if (scale != 0u) {
+        const float inv = __frcp_rn(e4m3_value(scale));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], inv);
+        codes = e2m1_pack8(x);
+      }
+    }
+    if (slot[u] >= 0 && !past) {
+      const int off = static_cast<int>(slot[u] & (g.page - 1));
+      uint8_t* blk = base + static_cast<size_t>(slot[u] >> g.page_log2) * page_bytes;
+      *reinterpret_cast<uint32_t*>(blk + off * (g.D / 2) + pc.part * 4) = codes;
+      uint8_t* sc = blk + g.ks + off * kv_scale_bytes(FMT, g.D);
+      if (pc.part % kLanes == 0) {
+        if (FMT == kFmtInt4)
+          *reinterpret_cast<uint16_t*>(sc + pc.part / kLanes * 2) = static_cast<uint16_t>(scale);
+        else
+          sc[pc.part / kLanes] = static_cast<uint8_t>(scale);
+      }
+    }
   }
 }
 
 // -------------------------------------------------------------------- read ---
-// One thread reads 16 codes (8 bytes) and their scale and writes the values
-// they stand for: code * scale, exact in fp32 (at most 3 + 11 bits) and, for
-// the E2M1 formats (2 + 4 bits), in bf16; INT4 in bf16 is rounded once.
-// A row with a slot below 0 or past the end is written as zeros.
-template <int FMT, typename Out>
+// A thread reads the codes of 16 output bytes (4 fp32 or 8 bf16 values) and
+// their scale and writes the values they stand for: code * scale, exact in fp32 (at
+// most 3 + 11 bits) and, for the E2M1 formats (2 + 4 bits), in bf16; INT4 in bf16 is
+// rounded once.  A row with a slot below 0 or past the end is written as zeros.
+template <int FMT, typename Out, int UNITS>
 __global__ void __launch_bounds__(kAppendThreads)
     kv_read_kernel(const KvGeom g, const long long* __restrict__ slots, int M, Out* __restrict__ k,
                    Out* __restrict__ v) {
   griddep_launch_dependents();
   griddep_wait();
-  const int per_head = g.D / 16;
-  const long long n = static_cast<long long>(M) * 2 * g.heads * per_head;
-  const long long idx = static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x;
-  if (idx >= n) return;
-  const int part = static_cast<int>(idx % per_head);
-  const long long hr = idx / per_head;
-  const int head2 = static_cast<int>(hr % (2 * g.heads));
-  const long long row = hr / (2 * g.heads);
-  const int side = head2 >= g.heads;
-  const int head = side ? head2 - g.heads : head2;
-  const long long slot = slots[row];
-  const bool past = slot >= g.num_pages * g.page;
-  if (past && part == 0 && head2 == 0) raise_error(kErrIndex);
-  float x[16];
+  constexpr int VALUES = 16 / sizeof(Out);
+  const Piece pc = piece_of_thread<VALUES, UNITS>(g);
+  long long slot[UNITS];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  if (slot >= 0 && !past) {
-    const long long page = slot >> g.page_log2;
-    const int off = static_cast<int>(slot & (g.page - 1));
-    const uint8_t* blk = g.pool + kv_block(g, page, head) + (side ? g.vc : 0);
-    const uint2 c = *reinterpret_cast<const uint2*>(blk + off * (g.D / 2) + part * 8);
-    const uint8_t* sc = blk + g.ks + off * kv_scale_bytes(FMT, g.D);
-    constexpr int kLanes = kv_group(FMT) / 16;
-    float s;
-    if (FMT == kFmtInt4)
-      s = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(sc + part / kLanes * 2)));
-    else
-      s = e4m3_value(sc[part / kLanes]);
-    const uint32_t w[2] = {c.x, c.y};
+  for (int u = 0; u < UNITS; ++u) {
+    const int row = pc.row + u * pc.step;
+    slot[u] = pc.row >= 0 && row < M ? slots[row] : -1;
+  }
+  const size_t page_bytes = static_cast<size_t>(g.heads) * g.head_bytes;
+  const uint8_t* base = g.pool + static_cast<size_t>(pc.head) * g.head_bytes + (pc.side ? g.vc : 0);
+  uint32_t c[UNITS];
+  float s[UNITS];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t nib = (w[i / 8] >> (4 * (i % 8))) & 15u;
-      const float val = FMT == kFmtInt4 ? static_cast<float>(static_cast<int>(nib << 28) >> 28) : e2m1_value(nib);
-      x[i] = __fmul_rn(val, s);
+  for (int u = 0; u < UNITS; ++u) {
+    const bool past = slot[u] >= g.num_pages * g.page;
+    if (past && pc.part == 0 && pc.head == 0) raise_error(kErrIndex);
+    c[u] = 0u;
+    s[u] = 0.f;
+    if (slot[u] >= 0 && !past) {
+      const int off = static_cast<int>(slot[u] & (g.page - 1));
+      const uint8_t* blk = base + static_cast<size_t>(slot[u] >> g.page_log2) * page_bytes;
+      const uint8_t* at = blk + off * (g.D / 2) + pc.part * (VALUES / 2);
+      c[u] = VALUES == 8 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
+      const uint8_t* sc = blk + g.ks + off * kv_scale_bytes(FMT, g.D);
+      const int group = pc.part * VALUES / kv_group(FMT);
+      if (FMT == kFmtInt4)
+        s[u] = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(sc + group * 2)));
+      else
+        s[u] = e4m3_value(sc[group]);
     }
   }
-  Out* dst = (side ? v : k) + (row * g.heads + head) * g.D + part * 16;
-  if constexpr (sizeof(Out) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<float4*>(dst)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-  } else {
-    uint32_t o[8];
+  for (int u = 0; u < UNITS; ++u) {
+    const int row = pc.row + u * pc.step;
+    if (pc.row < 0 || row >= M) break;
+    float x[VALUES];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int i = 0; i < VALUES; ++i) {
+      const uint32_t nib = (c[u] >> (4 * i)) & 15u;
+      const float val = FMT == kFmtInt4 ? static_cast<float>(static_cast<int>(nib << 28) >> 28) : e2m1_value(nib);
+      x[i] = __fmul_rn(val, s[u]);
+    }
+    Out* dst = (pc.side ? v : k) + (static_cast<long long>(row) * g.heads + pc.head) * g.D + pc.part * VALUES;
+    if constexpr (VALUES == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
 }
 

@@ -24,7 +24,7 @@
 namespace svdq {
 
 constexpr int kNormThreads = 128;
-constexpr int kNormBatch = 2;
+constexpr int kNormBatch = 4;
 
 struct NormRopeParams {
   const __nv_bfloat16* q;
@@ -50,97 +50,36 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& a, float2* v) {
   for (int i = 0; i < 4; ++i) v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
 }
 
-// `n` heads from `src` to `dst` (D elements apart; this lane's 8 elements of each); `n_warp` is the largest n in the warp.
-//   out = r (x A + x' B): x' the partner of x in its pair, A = w cos, B = -+ w' sin, r the head's 1 / rms.
-// A and B do not depend on the head, only on the row and on whether it is a query or a key.  BATCH heads
-// are loaded before the first is used.
+// out = r (x A + x' B): x' the partner of x in its pair, A = w cos, B = -+ w' sin, r the head's 1 / rms.
+// A and B do not depend on the head, only on the row and on whether it is a query or a key.  The next BATCH heads
+// are on their way while a batch is worked on, the first ones before the row's position is known.
 template <int LANES, bool INTERLEAVED, int BATCH>
-__device__ __forceinline__ void norm_rope_heads(const NormRopeParams& p, const __nv_bfloat16* src, __nv_bfloat16* dst, int n, int n_warp,
-                                                const __nv_bfloat16* w, bool mine, bool rotated, int l, int partner,
-                                                const float2 (&cs)[4], const float2 (&sn)[4]) {
-  float2 A[4], B[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = B[i] = make_float2(1.f, 1.f);
-  if (p.norm && w != nullptr && mine) {
-    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * l)), A);
-    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * partner)), B);
-    if (INTERLEAVED) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) B[i] = make_float2(B[i].y, B[i].x);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    A[i] = fmul2_rn(A[i], cs[i]);
-    B[i] = fmul2_rn(B[i], sn[i]);
-  }
-  const float inv_d = 1.f / static_cast<float>(p.D);
-  for (int j = 0; j < n_warp; j += BATCH, src += BATCH * p.D, dst += BATCH * p.D) {
-    uint4 raw[BATCH];
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b)
-      raw[b] = mine && j + b < n ? *reinterpret_cast<const uint4*>(src + b * p.D) : make_uint4(0u, 0u, 0u, 0u);
-    float ss[BATCH];
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      float2 x[4];
-      bf16x8_to_f32(raw[b], x);
-      float2 s2 = fmul2_rn(x[0], x[0]);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) s2 = ffma2(x[i], x[i], s2);
-      ss[b] = s2.x + s2.y;
-    }
-#pragma unroll
-    for (int o = 1; o < LANES; o *= 2)
-#pragma unroll
-      for (int b = 0; b < BATCH; ++b) ss[b] += __shfl_xor_sync(0xffffffffu, ss[b], o);
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      uint4 other;
-      if (INTERLEAVED) {
-        other = make_uint4(__byte_perm(raw[b].x, 0, 0x1032), __byte_perm(raw[b].y, 0, 0x1032), __byte_perm(raw[b].z, 0, 0x1032),
-                           __byte_perm(raw[b].w, 0, 0x1032));
-      } else {
-        other.x = __shfl_sync(0xffffffffu, raw[b].x, partner, LANES);
-        other.y = __shfl_sync(0xffffffffu, raw[b].y, partner, LANES);
-        other.z = __shfl_sync(0xffffffffu, raw[b].z, partner, LANES);
-        other.w = __shfl_sync(0xffffffffu, raw[b].w, partner, LANES);
-      }
-      if (!rotated) other = make_uint4(0u, 0u, 0u, 0u);     // those elements keep their values, infinities included
-      const float r = p.norm ? rsqrtf(ss[b] * inv_d + p.eps) : 1.f;
-      const float2 r2 = make_float2(r, r);
-      float2 x[4], y[4];
-      bf16x8_to_f32(raw[b], x);
-      bf16x8_to_f32(other, y);
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = fmul2_rn(ffma2(x[i], A[i], fmul2_rn(y[i], B[i])), r2);
-        o[i] = pack_bf16x2(t.x, t.y);
-      }
-      if (mine && j + b < n) *reinterpret_cast<uint4*>(dst + b * p.D) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-}
-
-template <int LANES, bool INTERLEAVED, int BATCH>
-__global__ void __launch_bounds__(kNormThreads, 8) qk_norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const NormRopeParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int group = static_cast<int>(blockIdx.x * kNormThreads + threadIdx.x) / LANES;
   const int l = threadIdx.x & (LANES - 1);
   const int row = group / p.chunks;
   const int h0 = (group - row * p.chunks) * p.chunk, h1 = min(h0 + p.chunk, p.q_heads + p.k_heads);
+  const bool there = row < p.rows && 8 * l < p.D;
+  const __nv_bfloat16* qrow = p.q + row * p.q_stride + 8 * l;
+  const __nv_bfloat16* krow = p.k + row * p.k_stride - static_cast<long long>(p.q_heads) * p.D + 8 * l;   // as if the keys followed the queries
+  uint4 ahead[BATCH];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b)
+      ahead[b] = there && h + b < h1 ? *reinterpret_cast<const uint4*>((h + b < p.q_heads ? qrow : krow) + (h + b) * p.D) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  load(h0);
   // A padded row (position below 0) is left as it is; every lane stays for the shuffles.
-  bool ok = row < p.rows;
+  bool mine = there;
   int pos = row;
-  if (ok && p.positions != nullptr) pos = p.positions[row];
-  if (ok && pos >= p.table_rows && p.rot > 0) {
+  if (row < p.rows && p.positions != nullptr) pos = p.positions[row];
+  if (row < p.rows && pos >= p.table_rows && p.rot > 0) {
     if (l == 0) raise_error(kErrIndex);
-    ok = false;
+    mine = false;
   }
-  if (pos < 0) ok = false;
-  const bool mine = ok && 8 * l < p.D;
+  if (pos < 0) mine = false;
 
   const int half = p.rot / 2;
   const bool rotated = 8 * l < p.rot;
@@ -174,16 +113,77 @@ __global__ void __launch_bounds__(kNormThreads, 8) qk_norm_rope_kernel(const Nor
       }
     }
   }
-  // The bounds of the loops are those of the whole warp: its shuffles need every lane.
-  const int nq = max(0, min(h1, p.q_heads) - h0), k0 = max(h0, p.q_heads), nk = max(0, h1 - k0);
-  const int nq_warp = LANES == 32 ? nq : __reduce_max_sync(0xffffffffu, nq), nk_warp = LANES == 32 ? nk : __reduce_max_sync(0xffffffffu, nk);
-  if (nq_warp > 0)
-    norm_rope_heads<LANES, INTERLEAVED, BATCH>(p, p.q + row * p.q_stride + h0 * p.D + 8 * l, p.q_out + row * p.q_out_stride + h0 * p.D + 8 * l,
-                                               nq, nq_warp, p.q_weight, mine, rotated, l, partner, cs, sn);
-  if (nk_warp > 0)
-    norm_rope_heads<LANES, INTERLEAVED, BATCH>(p, p.k + row * p.k_stride + (k0 - p.q_heads) * p.D + 8 * l,
-                                               p.k_out + row * p.k_out_stride + (k0 - p.q_heads) * p.D + 8 * l, nk, nk_warp, p.k_weight,
-                                               mine, rotated, l, partner, cs, sn);
+  const float inv_d = 1.f / static_cast<float>(p.D);
+  __nv_bfloat16* qout = p.q_out + row * p.q_out_stride + 8 * l;
+  __nv_bfloat16* kout = p.k_out + row * p.k_out_stride - static_cast<long long>(p.q_heads) * p.D + 8 * l;
+  float2 A[4], B[4];
+  int kind = -1;                             // of A and B: 0 queries, 1 keys
+  for (int j = 0; j < p.chunk; j += BATCH) { // the same count for every lane of a warp
+    uint4 raw[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) raw[b] = ahead[b];
+    if (j + BATCH < p.chunk) load(h0 + j + BATCH);
+    float ss[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      float2 x[4];
+      bf16x8_to_f32(raw[b], x);
+      float2 s2 = fmul2_rn(x[0], x[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) s2 = ffma2(x[i], x[i], s2);
+      ss[b] = s2.x + s2.y;
+    }
+#pragma unroll
+    for (int o = 1; o < LANES; o *= 2)
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) ss[b] += __shfl_xor_sync(0xffffffffu, ss[b], o);
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int h = h0 + j + b;
+      if (kind != (h < p.q_heads ? 0 : 1)) {
+        kind = h < p.q_heads ? 0 : 1;
+        const __nv_bfloat16* w = kind == 0 ? p.q_weight : p.k_weight;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A[i] = B[i] = make_float2(1.f, 1.f);
+        if (p.norm && w != nullptr && mine) {
+          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * l)), A);
+          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(w + 8 * partner)), B);
+          if (INTERLEAVED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) B[i] = make_float2(B[i].y, B[i].x);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          A[i] = fmul2_rn(A[i], cs[i]);
+          B[i] = fmul2_rn(B[i], sn[i]);
+        }
+      }
+      uint4 other;
+      if (INTERLEAVED) {
+        other = make_uint4(__byte_perm(raw[b].x, 0, 0x1032), __byte_perm(raw[b].y, 0, 0x1032), __byte_perm(raw[b].z, 0, 0x1032),
+                           __byte_perm(raw[b].w, 0, 0x1032));
+      } else {
+        other.x = __shfl_sync(0xffffffffu, raw[b].x, partner, LANES);
+        other.y = __shfl_sync(0xffffffffu, raw[b].y, partner, LANES);
+        other.z = __shfl_sync(0xffffffffu, raw[b].z, partner, LANES);
+        other.w = __shfl_sync(0xffffffffu, raw[b].w, partner, LANES);
+      }
+      if (!rotated) other = make_uint4(0u, 0u, 0u, 0u);     // those elements keep their values, infinities included
+      const float r = p.norm ? rsqrtf(ss[b] * inv_d + p.eps) : 1.f;
+      const float2 r2 = make_float2(r, r);
+      float2 x[4], y[4];
+      bf16x8_to_f32(raw[b], x);
+      bf16x8_to_f32(other, y);
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = fmul2_rn(ffma2(x[i], A[i], fmul2_rn(y[i], B[i])), r2);
+        o[i] = pack_bf16x2(t.x, t.y);
+      }
+      if (mine && h < h1) *reinterpret_cast<uint4*>((kind == 0 ? qout : kout) + h * p.D) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 }  // namespace svdq
