@@ -585,12 +585,46 @@ def _oracle_step(O, spec, prep, wq, sample, bias):
     O.linear(spec.fmt, act, wq, prep["L2"] if prep["rank"] else None, bias, spec.N)
 
 
+def block_attention(S, M, qkv, out_features, fmt, dev):
+    """The attention between a block's qkv and out layers, as one call on the
+    qkv layer's output: plan of one request of M new tokens, query/key norm and
+    rotation in place, keys and values into a 4-bit cache, every token attending to
+    every token.  Returns (step, output M x out_features, FLOP, launches)."""
+    dim = 128
+    heads = out_features // dim
+    if qkv.shape[1] != 3 * heads * dim:
+        raise SystemExit("--attention needs a qkv layer of three times the out layer's inputs, in heads of 128")
+    page = 128
+    rows = qkv.view(M, 3 * heads, dim)
+    q, k, v = rows[:, :heads], rows[:, heads:2 * heads], rows[:, 2 * heads:]
+    pages = (M + page - 1) // page
+    cache = S.KVCache(fmt, heads, dim, page, num_pages=pages)
+    table = torch.full((1, pages), -1, dtype=torch.int32, device=dev)
+    free = torch.arange(pages, dtype=torch.int32, device=dev)
+    new = torch.tensor([M], dtype=torch.int32, device=dev)
+    none = torch.zeros(1, dtype=torch.int32, device=dev)
+    angle = torch.arange(M, dtype=torch.float64)[:, None] * 10000.0 ** (-2.0 * torch.arange(dim // 2, dtype=torch.float64) / dim)
+    rope = torch.cat((angle.cos(), angle.sin()), 1).float().to(dev)
+    ones = torch.ones(dim, dtype=torch.bfloat16, device=dev)
+    out = torch.empty(M, heads, dim, dtype=torch.bfloat16, device=dev)
+
+    def step():
+        cu, lens, pos, slots, _ = S.svdq_kv_plan(new, none, table, free, M, page)
+        S.svdq_qk_norm_rope(q, k, rope, pos, ones, ones, interleaved=True, q_out=q, k_out=k)
+        S.svdq_kv_append(cache, k, v, slots)
+        S.svdq_kv_attention(cache, q, cu, lens, table, causal=False, out=out)
+
+    return step, out.view(M, heads * dim), 4.0 * dim * heads * M * M, 4
+
+
 def run_block(args):
     """--layer all: the workload's layers back to back as one step (one DiT
     block's four linears at M tokens, each on its own seeded input), under one
     event pair with the L2 flushed before every step.  The activation kernel of
     each layer is launched while the previous GEMM drains (programmatic
-    dependent launch).  Reports the block and each layer's share."""
+    dependent launch).  Reports the block and each layer's share.
+    --attention puts the block's attention between its qkv and out layers: it
+    works on the one's output, and the other on its own."""
     import w4a4_gemm_b200 as S
 
     world, rank, local = dist_env()
@@ -614,6 +648,16 @@ def run_block(args):
         del W
     flush = torch.empty(FLUSH_BYTES // 4, dtype=torch.float32, device=dev)
     stream = torch.cuda.current_stream()
+    attend, attn_flops, attn_launches, attn_after = None, 0.0, 0, -1
+    if args.attention:
+        names = [s.name for s, *_ in layers]
+        if "qkv" not in names or names.index("qkv") + 1 >= len(names) or names[names.index("qkv") + 1] != "out":
+            raise SystemExit("--attention needs a config with a qkv layer and its out layer (c5_block)")
+        attn_after = names.index("qkv")
+        attend, attn_out, attn_flops, attn_launches = block_attention(S, M, layers[attn_after][4], layers[attn_after + 1][0].K,
+                                                                      args.kv_fmt, dev)
+        spec, w, _, ws, Y = layers[attn_after + 1]
+        layers[attn_after + 1] = (spec, w, attn_out, ws, Y)
 
     def block(evs=None, split=False):
         for i, (spec, w, X, ws, Y) in enumerate(layers):
@@ -621,6 +665,8 @@ def run_block(args):
                 evs[i].record(stream)
             S.svdq_quantize_act(w, X, ws)
             S.svdq_linear(w, ws, M, Y)
+            if i == attn_after:
+                attend()
         if evs is not None:
             evs[-1].record(stream)
 
@@ -656,7 +702,7 @@ def run_block(args):
         raise RuntimeError("device wait timed out during timing")
     t_block = np.array([e[0].elapsed_time(e[n]) for e in whole]) * 1e-3
     t_layer = np.array([[e[i].elapsed_time(e[i + 1]) for i in range(n)] for e in split]).mean(axis=0) * 1e-3
-    flops = sum(2.0 * M * spec.K * spec.N for spec, *_ in layers)
+    flops = sum(2.0 * M * spec.K * spec.N for spec, *_ in layers) + attn_flops
     total = float(t_block.sum())
     (total,) = max_over_ranks([total], world, dev)
     pk = peaks()
@@ -674,9 +720,12 @@ def run_block(args):
         "us_split_how": "us_per_block: the block under one event pair; us_per_layer_in_block: a second pass "
                         "with an event before every layer",
         "pct_fp4_peak_block": round(100.0 * flops / (total / args.steps) / 1e12 / (pk["bf16"] * 4.0), 2),
-        "gpu_launches": 2 * n * args.steps,
+        "gpu_launches": (2 * n + attn_launches) * args.steps,
         "clocks": clocks,
     }
+    if attend is not None:
+        line["config"]["attention"] = f"between qkv and out, counted with qkv: {args.kv_fmt} cache, every token to every token"
+        line["attention_flop"] = attn_flops
     if rank == 0:
         print(json.dumps(line), flush=True)
     for _, w, *_ in layers:
@@ -754,11 +803,16 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--rank-sweep", type=lambda v: [int(x) for x in v.split(",")], default=None,
                     help="also time the layer at these ranks, e.g. 16,32,48,64")
+    ap.add_argument("--attention", action="store_true",
+                    help="with --layer all: the block's attention over a 4-bit cache between its qkv and out layers")
+    ap.add_argument("--kv-fmt", choices=["nvfp4", "int4", "fp4g32"], default="nvfp4", help="the cache's format")
     ap.add_argument("--no-extras", action="store_true",
                     help="skip the rank-0 comparison and the tensor-ceiling measurement")
     args = ap.parse_args()
     if args.warmup < 3:
         ap.error("--warmup must be >= 3")
+    if args.attention and args.layer != "all":
+        ap.error("--attention goes with --layer all")
     if args.impl == "reference":
         run_reference(args)
     elif args.layer == "all":

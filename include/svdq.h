@@ -395,10 +395,12 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
  * weights exp(s - max) are rounded to fp16 for the product with the values.
  * Rows outside cu_q[0] .. cu_q[batch] - 1 are left as they are.  What the cache holds past
  * kv_lens[b] is never used, whatever its bytes.  Out of range (bit 3): cu_q is
- * clamped to 0 .. rows, kv_lens to what the table row holds, and the keys of a page
+ * clamped to 0 .. rows, kv_lens to what the table row holds (and 2^30 - 65536), and the keys of a page
  * outside the pool are masked.  `workspace` (svdq_kv_attention_workspace_bytes,
  * 256-byte aligned, no initial contents) is scratch of this call: calls that may
- * overlap on the GPU need one each.  batch <= 65536. */
+ * overlap on the GPU need one each.  (After a wait of a captured call ran out, bit 4,
+ * zero the workspace before its graph is replayed: the count of that replay's
+ * finished parts is in it.)  batch <= 65536, rows * q_heads / kv_heads < 2^30 - 65536. */
 typedef struct {
   svdq_kv_cache cache;
   const void* q;           /* bf16 rows x q_heads x head_dim */

@@ -400,3 +400,150 @@ def test_serving_steps(S, fmt):
             at += n
         assert (out[at:] == 0).all()
     wqkv.close(), wout.close()
+
+
+# ------------------------------------------------------ longer, split, together ---
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,hq,hk,lens", [
+    (128, 4, 2, [(700, 2500), (1, 3000), (333, 900)]), (64, 6, 2, [(500, 1700), (64, 64)]), (128, 1, 1, [(1200, 1200)]),
+    (128, 8, 1, [(1, 20000)]), (64, 4, 1, [(1, 9000), (1, 1)]), (128, 9, 3, [(3, 5000), (2, 700)])])
+def test_attention_split_items(S, fmt, D, hq, hk, lens):
+    """Items cut between many CTAs, by both kernels, causal and with a window that skips whole tiles."""
+    b = R.Batch(fmt, D, 64, hq, hk, lens, seed=31)
+    attend(S, b)
+    attend(S, b, window=300)
+
+
+def test_attention_many_requests(S):
+    """More requests than a scan's first level, most of them without new tokens."""
+    rng = np.random.default_rng(5)
+    lens = [(int(n), int(n) + int(kv)) for n, kv in zip(rng.integers(0, 3, 1500) * (rng.random(1500) < 0.3), rng.integers(0, 60, 1500))]
+    attend(S, R.Batch("nvfp4", 64, 16, 4, 2, lens, seed=6))
+
+
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 900)], [(90, 700), (200, 900)]])
+def test_attention_on_two_streams_at_once(S, lens):
+    """Two calls in flight together, each with its own workspace, give what each gives alone."""
+    batches = [R.Batch("nvfp4", 128, 64, 8, 2, lens, seed=s) for s in (40, 41)]
+    want = [attend(S, b)[0] for b in batches]
+    args = [(cache_of(S, b), b.q.cuda(), dev(b.cu), dev([kv for _, kv in b.lens], torch.int32), dev(b.table)) for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in (0, 1):
+            got[i].append(S.svdq_kv_attention(*args[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+    assert S.svdq_get_error() == 0
+
+
+def test_step_in_a_graph(S):
+    """Plan, norm, append and attention of a decode step captured once and replayed as the requests grow."""
+    hq, hk, D, page, batch = 8, 2, 64, 16, 3
+    g = torch.Generator().manual_seed(9)
+    cache = S.KVCache("nvfp4", hk, D, page, num_pages=24)
+    table = torch.full((batch, 8), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(24, dtype=torch.int32, device="cuda")
+    ones, lens = torch.ones(batch, dtype=torch.int32, device="cuda"), torch.zeros(batch, dtype=torch.int32, device="cuda")
+    taken = torch.zeros(1, dtype=torch.int64, device="cuda")
+    qkv = torch.zeros(batch, hq + 2 * hk, D, dtype=torch.bfloat16, device="cuda")
+    rope = dev(R.rotation(128, D))
+    out = torch.zeros(batch, hq, D, dtype=torch.bfloat16, device="cuda")
+    q_out, k_out = torch.zeros_like(out), torch.zeros(batch, hk, D, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        cu, total, pos, slots, used = S.svdq_kv_plan(ones, lens, table, torch.roll(free, 0)[:24], batch, page)
+        S.svdq_qk_norm_rope(qkv[:, :hq], qkv[:, hq:hq + hk], rope, pos, q_out=q_out, k_out=k_out)
+        S.svdq_kv_append(cache, k_out, qkv[:, hq + hk:], slots)
+        S.svdq_kv_attention(cache, q_out, cu, total, table, out=out)
+        lens.copy_(total)
+        taken.add_(used)
+        free.copy_(free[(torch.arange(24, device="cuda") + used) % 24])      # the taken pages go to the end
+
+    step()                                            # sets kernel attributes; then start over
+    torch.cuda.synchronize()
+    table.fill_(-1), lens.zero_(), taken.zero_(), free.copy_(torch.arange(24, dtype=torch.int32))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    held = [[np.zeros((0, hk, D))] * 2 for _ in range(batch)]
+    for i in range(40):
+        x = torch.randn(batch, hq + 2 * hk, D, generator=g).to(torch.bfloat16)
+        qkv.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(batch):
+            for side, t in enumerate((k_out, x[:, hq + hk:])):
+                held[b][side] = np.concatenate((held[b][side], R.quantize("nvfp4", t[b:b + 1].cpu())[2]))
+            o, _, to, _ = R.attention(q_out[b:b + 1].double().cpu().numpy(), *held[b], D ** -0.5, True, 0)
+            within(out[b:b + 1], o, to)
+    assert S.svdq_get_error() == 0 and lens.tolist() == [40] * 3 and int(taken) == 9
+
+
+@pytest.mark.parametrize("lens", [[(1, 3000), (1, 500)], [(300, 900)]])
+def test_attention_wait_expiry_is_reported_and_recovered(S, lens):
+    """Budget of one cycle: waits that outlast their first poll (the hardware holds one for a while) run out,
+    the error word says so (bit 4 alone), and with the budget restored the same call gives the same bits again."""
+    b = R.Batch("nvfp4", 128, 64, 8, 2, lens, seed=14)
+    want, _ = attend(S, b)
+    args = (cache_of(S, b), b.q.cuda(), dev(b.cu), dev([kv for _, kv in b.lens], torch.int32), dev(b.table))
+    try:
+        S.svdq_set_wait_budget(1)
+        for _ in range(10):
+            S.svdq_kv_attention(*args)
+            err = S.svdq_get_error()
+            assert err >= 0 and (err & ~16) == 0, err
+    finally:
+        S.svdq_set_wait_budget(1 << 31)
+    again = S.svdq_kv_attention(*args)
+    torch.cuda.synchronize()
+    assert S.svdq_get_error() == 0 and torch.equal(again, want)
+
+
+def test_refused_tensors(S):
+    """What the Python calls refuse before anything is launched."""
+    c = S.KVCache("nvfp4", 2, 64, 16, num_pages=4)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        S.svdq_kv_append(c, x.half(), x, slots)
+    with pytest.raises(TypeError):
+        S.svdq_kv_append(c, x.cpu(), x, slots)
+    with pytest.raises(TypeError):
+        S.svdq_kv_append(c, x, x, slots.int())
+    with pytest.raises(ValueError):
+        S.svdq_kv_append(c, x, x, slots[:2])
+    with pytest.raises(ValueError):
+        S.svdq_kv_append(c, x.transpose(1, 2).contiguous().transpose(1, 2), x, slots)      # heads not contiguous
+    with pytest.raises(ValueError):
+        S.svdq_kv_append(c, torch.zeros(400, dtype=torch.bfloat16, device="cuda")[1:385].view(3, 2, 64), x, slots)   # 2-byte start
+    with pytest.raises(TypeError):
+        S.svdq_kv_read(c, slots, torch.float16)
+    with pytest.raises(ValueError):
+        S.svdq_kv_attention(c, x, i32(0, 3), i32(3, 3), table)
+    with pytest.raises(ValueError):
+        S.svdq_kv_attention(c, x, i32(0, 3), i32(3), table, out=x[:1].expand(3, 2, 64))     # rows of the output overlap
+    with pytest.raises(ValueError):
+        S.svdq_kv_attention(c, x, i32(0, 3), i32(3), table, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(S.SvdqError):
+        S.svdq_kv_attention(c, torch.zeros(3, 3, 64, dtype=torch.bfloat16, device="cuda"), i32(0, 3), i32(3), table)
+    with pytest.raises(S.SvdqError):
+        S.svdq_kv_attention(c, x, i32(0, 3), i32(3), table, window=-1)
+    with pytest.raises(S.SvdqError):
+        S.svdq_kv_attention(c, x, i32(0, 3), i32(3), table, scale=float("nan"))
+    with pytest.raises(ValueError):
+        S.svdq_kv_plan(i32(1), i32(1, 2), table, i32(1), 1, 16)
+    with pytest.raises(S.SvdqError):
+        S.svdq_kv_plan(i32(1), i32(1), table, i32(1), 1, 24)
+    with pytest.raises(ValueError):
+        S.svdq_qk_norm_rope(x, x, torch.zeros(4, 64, device="cuda"), i32(0))
+    with pytest.raises(S.SvdqError):
+        S.svdq_qk_norm_rope(x, x, torch.zeros(2, 64, device="cuda"))        # fewer table rows than rows
+    with pytest.raises(ValueError):
+        S.KVCache("nvfp4", 2, 64, 16, torch.zeros(4, 2, 100, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert S.svdq_get_error() == 0

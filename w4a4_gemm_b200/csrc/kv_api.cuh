@@ -346,7 +346,7 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
       (d->table_width > 0 && d->block_table == nullptr) ||
       (d->rows > 1 && d->out_stride < static_cast<long long>(d->q_heads) * p.g.D))
     return SVDQ_ERR_INVALID_ARG;
-  if (d->batch > kAttnMaxBatch || static_cast<long long>(d->rows) * (d->q_heads / p.g.heads) > 0x7fff0000LL) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (d->batch > kAttnMaxBatch || static_cast<long long>(d->rows) * (d->q_heads / p.g.heads) > kMaxKeys) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (d->workspace == nullptr || (reinterpret_cast<uintptr_t>(d->workspace) & 255u)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
@@ -365,7 +365,7 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
   p.q_heads = d->q_heads;
   p.rep = fast_div(d->q_heads / p.g.heads);
   p.causal = d->causal != 0;
-  p.window = d->window;
+  p.window = static_cast<int>(std::min<long long>(d->window, kMaxKeys + 1));   // longer windows see every key alike
   p.scale = d->scale;
   p.budget = wait_budget();
   p.nonce = launch_nonce();

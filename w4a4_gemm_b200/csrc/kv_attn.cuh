@@ -493,10 +493,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
   float* row_sum = row_max + WARPS * RT;
   __shared__ Share share;
   __shared__ int last_flag;
-  __shared__ int claims[2];                           // steps of the segment that warps have taken; two segments in turn
 
   griddep_launch_dependents();
-  if (threadIdx.x < 2) claims[threadIdx.x] = 0;
   if (lane == 0) {
     for (int s = 0; s < kDecStages; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
@@ -511,7 +509,6 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
   Request req = load_request(p, b);
   uint32_t phase = 0;                                 // bit s: parity of stage s
   bool dead = false;                                  // a wait ran out
-  uint32_t seg = 0;
 
   // Pieces of a step that lie in one page are copied by lanes 0 .. pieces - 1.
   const int piece_log2 = min(p.g.page_log2, 6);
@@ -527,15 +524,13 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
     const int first = k0 + unit * UNIT;           // keys of this segment
     const int limit = here >= units - unit ? k1 : first + here * UNIT;
     const int* table = p.table + b * p.table_stride;
-    // Steps go to whichever warp is next: the scheduler serves older warps first, and equal shares would leave the
-    // others alone at the end.
+    // The warps take turns along the keys, in an order that does not change from run to run: nor do the sums.
+    int key = first + warp * kDecChunk;
     auto claim = [&]() {
-      int c = 0;
-      if (lane == 0) c = atomicAdd(&claims[seg & 1], 1);
-      const long long key = first + static_cast<long long>(__shfl_sync(0xffffffffu, c, 0)) * kDecChunk;
-      return key < limit ? static_cast<int>(key) : -1;      // first key of the step, or none left
+      const int c = key < limit ? key : -1;           // first key of the step, or none left
+      key += UNIT;
+      return c;
     };
-
     // The page of this lane's piece of the step at `next`: -1 past the end, or outside the pool.
     auto page_of = [&](int key0) {
       const int key = key0 + (lane << piece_log2);
@@ -748,8 +743,6 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
     }
 
     // ------------------------------------------------ the next item of the share
-    if (threadIdx.x == 0) claims[seg & 1] = 0;        // every warp is past its last claim of this segment
-    ++seg;
     count -= here;
     at += here;
     if (count <= 0) break;

@@ -60,6 +60,9 @@ struct AttnParams {
   long long budget;              // of a bounded wait, in cycles
 };
 
+// Keys of a request; rows and windows are cut to it too, so that positions stay far inside 32 bits.
+constexpr long long kMaxKeys = (1ll << 30) - 65536;
+
 struct Request {
   int row0, n, kv;               // first row, new tokens, keys
 };
@@ -67,7 +70,7 @@ struct Request {
 // Lengths as the caller gives them, cut to what the rows and the table hold.
 __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
   const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], kv = p.kv_lens[b];
-  const long long cap = min(static_cast<long long>(p.width) << p.g.page_log2, 0x7fff0000LL);
+  const long long cap = min(static_cast<long long>(p.width) << p.g.page_log2, kMaxKeys);
   Request r;
   r.row0 = min(max(c0, 0), p.rows);
   r.n = min(max(c1, r.row0), p.rows) - r.row0;
