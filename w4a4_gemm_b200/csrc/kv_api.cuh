@@ -214,7 +214,7 @@ SVDQ_API int svdq_kv_plan(const svdq_kv_plan_desc* d, void* stream) {
   p.positions = d->positions;
   p.slots = reinterpret_cast<long long*>(d->slots);
   p.used = d->used;
-  const int ctas = std::max(1, (d->rows + kPlanRows - 1) / kPlanRows);
+  const int ctas = std::max({1, (d->rows + kPlanRows - 1) / kPlanRows, (d->batch + kPlanRequests - 1) / kPlanRequests});
   const size_t smem = (2 * static_cast<size_t>(d->batch) + 1) * sizeof(int);
   SVDQ_CUDA(launch_pdl(kv_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, static_cast<cudaStream_t>(stream), 0u, p));
   return SVDQ_OK;

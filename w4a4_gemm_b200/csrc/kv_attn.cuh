@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
     fence_barrier_init();
   }
   griddep_wait();
-  find_share<RT, UNIT>(p, reinterpret_cast<long long*>(dec_smem), &share);
+  find_share<RT, UNIT, false>(p, reinterpret_cast<long long*>(dec_smem), &share);
   fence_proxy_async_smem();                           // the scan's words lie under the rings
   int count = share.count;
   if (count == 0) return;
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
     constexpr int SLOT = RT * (D + 2);
     const float* all = reinterpret_cast<const float*>(dec_smem);
     constexpr int kWarpFloats = kDecStages * STAGE / 4;
-    float* slot = p.partials + (2ll * blockIdx.x + (at == share.begin ? 0 : 1)) * SLOT;
+    float* slot = p.partials + (2ll * blockIdx.x + (unit == 0 ? 1 : 0)) * SLOT;
     for (int e = threadIdx.x; e < live_rows * Q; e += (32 * WARPS)) {
       const int row = e / Q, d = e % Q * 4;
       float top = row_max[row];
@@ -711,7 +711,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
     }
     if (split) {
       const long long item = at - unit;               // unit number of the item's first unit
-      const int c0 = share_of(share.base, share.rem, item), c1 = share_of(share.base, share.rem, item + units - 1);
+      int c0, c1;
+      item_parts(share, item, units, c0, c1);
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
       }
       __syncthreads();
       if (last_flag) {
-        const float* part0 = p.partials + (share_begin(share.base, share.rem, c0) == item ? 2ll * c0 : 2ll * c0 + 1) * SLOT;
+        const float* part0 = p.partials + (2ll * c0 + 1) * SLOT;
         for (int e = threadIdx.x; e < live_rows * Q; e += (32 * WARPS)) {
           const int row = e / Q, d = e % Q * 4;
           float top = -INFINITY, sum = 0.f;

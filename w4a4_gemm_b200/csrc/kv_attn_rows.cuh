@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
     tmem_relinquish();
   }
   griddep_wait();
-  find_share<RT, KT>(p, reinterpret_cast<long long*>(smem), &share);
+  find_share<RT, KT, true>(p, reinterpret_cast<long long*>(smem), &share);
   fence_proxy_async_smem();                           // the scan's words lie under Q
   tc_fence_before();
   __syncthreads();
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         __syncwarp();
       };
       // a partial result: [D / 4][256] float4, so that the lanes of a store are neighbours; then [256] (max, sum)
-      float4* slot = reinterpret_cast<float4*>(p.partials + (2ll * blockIdx.x + (w.at == share.begin ? 0 : 1)) * SLOT);
+      float4* slot = reinterpret_cast<float4*>(p.partials + (2ll * blockIdx.x + (w.unit == 0 ? 1 : 0)) * SLOT);
       const int srow = half * 128 + lrow;
       const float inv = l > 0.f ? unscale / l : 0.f;
 #pragma unroll
@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         __stcg(reinterpret_cast<float2*>(slot + RT * (D / 4)) + srow, make_float2(m, l));
         // each half of an item is joined by itself, by the CTA whose four warps arrive last
         const long long item = w.at - w.unit;
-        const int c0 = share_of(share.base, share.rem, item), c1 = share_of(share.base, share.rem, item + w.units - 1);
+        int c0, c1;
+        item_parts(share, item, w.units, c0, c1);
         __threadfence();
         if (!meet(&join[half], 0)) break;
         if ((warp & 3) == 0 && lane == 0) {
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         }
         if (!meet(&join[half], 1)) break;
         if (last_flag[half]) {
-          const float* part0 = p.partials + (share_begin(share.base, share.rem, c0) == item ? 2ll * c0 : 2ll * c0 + 1) * SLOT;
+          const float* part0 = p.partials + (2ll * c0 + 1) * SLOT;
           auto part = [&](int c) { return reinterpret_cast<const float4*>(c == c0 ? part0 : p.partials + 2ll * c * SLOT); };
           float top = -INFINITY, total = 0.f;
           for (int c = c0; c <= c1; ++c) {

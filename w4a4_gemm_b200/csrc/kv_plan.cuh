@@ -24,6 +24,7 @@ namespace svdq {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanRows = 1024;            // rows of positions and slots per CTA
+constexpr int kPlanRequests = 64;          // requests whose results a CTA writes, a warp each
 constexpr int kPlanMaxRequests = 16384;    // 8 bytes of shared memory each
 
 struct PlanParams {

@@ -151,6 +151,7 @@ struct Share {
   long long base;                // units of a CTA's share; the first `rem` CTAs have one more
   long long begin;               // first unit of this CTA
   int rem;
+  int snap;                      // see find_share
   int count;                     // units of this CTA (0: none)
   int b, h, rt, unit;            // the item of the first unit, and the unit inside it
 };
@@ -167,8 +168,71 @@ __device__ __forceinline__ int share_of(long long base, int rem, long long u) {
   return static_cast<int>(u < head ? div_units(u, base + 1) : rem + div_units(u - head, base));
 }
 
-// Called by all threads.  `sums` holds (batch + 31) / 32 words of shared memory.
+// Where unit u lies, found by one warp from the 32 requests in its lanes' `one` and `r` (groups == 1) or from
+// the sums of 32 requests each.
+struct Place {
+  int b, h, rt, unit, units;     // the item, the unit inside it, its units
+};
 template <int RT, int KT>
+__device__ __forceinline__ Place find_unit(const AttnParams& p, const long long* sums, int groups, Request r, long long one, long long left) {
+  const int lane = threadIdx.x & 31;
+  int g = 0;
+  if (groups > 1) {
+    // the group of 32 requests that holds it
+    for (int base = 0;; base += 32) {
+      const long long v = base + lane < groups ? sums[base + lane] : 0;
+      const long long inc = warp_inclusive(v);
+      const unsigned over = __ballot_sync(0xffffffffu, inc > left);
+      if (over) {
+        const int k = __ffs(over) - 1;
+        left -= __shfl_sync(0xffffffffu, inc - v, k);
+        g = base + k;
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, inc, 31);
+      if (base + 32 >= groups) break;         // not reached: u < total
+    }
+    one = group_units<RT, KT>(p, 32 * g, r);
+  }
+  // the request, the key head, the row tile
+  const long long v = one * p.g.heads, inc = warp_inclusive(v);
+  const unsigned over = __ballot_sync(0xffffffffu, inc > left);
+  const int k = over ? __ffs(over) - 1 : 0;
+  left -= __shfl_sync(0xffffffffu, inc - v, k);
+  const long long per_head = max(1LL, __shfl_sync(0xffffffffu, one, k));
+  Request o;
+  o.row0 = 0;
+  o.n = __shfl_sync(0xffffffffu, r.n, k);
+  o.kv = __shfl_sync(0xffffffffu, r.kv, k);
+  Place at;
+  at.b = 32 * g + k;
+  at.h = static_cast<int>(div_units(left, per_head));
+  left -= at.h * per_head;
+  const int tiles = row_tiles<RT>(p, o);
+  at.rt = 0;
+  if (tiles > 1) {
+    for (int base = 0; base < tiles; base += 32) {
+      const long long w = base + lane < tiles ? tile_units<RT, KT>(p, o, base + lane) : 0;
+      const long long winc = warp_inclusive(w);
+      const unsigned past = __ballot_sync(0xffffffffu, winc > left);
+      if (past) {
+        const int j = __ffs(past) - 1;
+        left -= __shfl_sync(0xffffffffu, winc - w, j);
+        at.rt = base + j;
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, winc, 31);
+    }
+  }
+  at.unit = static_cast<int>(left);
+  at.units = tiles > 0 ? tile_units<RT, KT>(p, o, at.rt) : 1;
+  return at;
+}
+
+// Called by all threads.  `sums` holds (batch + 31) / 32 words of shared memory.
+// SNAP: a boundary between shares that lies within share.snap units of an item's end moves there (an eighth of a
+// share at most: a cut costs both sides a partial result, about three units of the many-row kernel).
+template <int RT, int KT, bool SNAP>
 __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums, Share* s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (p.batch + 31) / 32;
@@ -192,73 +256,45 @@ __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums,
     } else {
       const long long each = div_units(total, ctas);
       const int rem = static_cast<int>(total - each * ctas);
-      const long long begin = share_begin(each, rem, c), end = share_begin(each, rem, c + 1);
-      long long left = begin;
-      int g = 0;
-      if (groups > 1) {
-        // the group of 32 requests that holds `begin`
-        for (int base = 0;; base += 32) {
-          const long long v = base + lane < groups ? sums[base + lane] : 0;
-          const long long inc = warp_inclusive(v);
-          const unsigned over = __ballot_sync(0xffffffffu, inc > left);
-          if (over) {
-            const int k = __ffs(over) - 1;
-            left -= __shfl_sync(0xffffffffu, inc - v, k);
-            g = base + k;
-            break;
-          }
-          left -= __shfl_sync(0xffffffffu, inc, 31);
-          if (base + 32 >= groups) break;     // not reached: begin < total
-        }
-        one = group_units<RT, KT>(p, 32 * g, r);
-      }
-      // the request, the key head, the row tile
-      const long long v = one * p.g.heads, inc = warp_inclusive(v);
-      const unsigned over = __ballot_sync(0xffffffffu, inc > left);
-      const int k = over ? __ffs(over) - 1 : 0;
-      left -= __shfl_sync(0xffffffffu, inc - v, k);
-      const long long per_head = max(1LL, __shfl_sync(0xffffffffu, one, k));
-      Request o;
-      o.row0 = 0;
-      o.n = __shfl_sync(0xffffffffu, r.n, k);
-      o.kv = __shfl_sync(0xffffffffu, r.kv, k);
-      const int h = static_cast<int>(div_units(left, per_head));
-      left -= h * per_head;
-      const int tiles = row_tiles<RT>(p, o);
-      int rt = 0;
-      if (tiles > 1) {
-        for (int base = 0; base < tiles; base += 32) {
-          const long long w = base + lane < tiles ? tile_units<RT, KT>(p, o, base + lane) : 0;
-          const long long winc = warp_inclusive(w);
-          const unsigned past = __ballot_sync(0xffffffffu, winc > left);
-          if (past) {
-            const int j = __ffs(past) - 1;
-            left -= __shfl_sync(0xffffffffu, winc - w, j);
-            rt = base + j;
-            break;
-          }
-          left -= __shfl_sync(0xffffffffu, winc, 31);
-        }
+      const int snap = SNAP ? static_cast<int>(min(each / 8, 64LL)) : 0;
+      long long begin = share_begin(each, rem, c), end = share_begin(each, rem, c + 1);
+      Place at = find_unit<RT, KT>(p, sums, groups, r, one, begin);
+      if (SNAP) {
+        auto moved = [&](const Place& w) {    // by how much the boundary at w moves
+          const int back = w.unit, on = w.units - w.unit;
+          return min(back, on) > snap || back == 0 ? 0 : back <= on ? -back : on;
+        };
+        const int d = moved(at);
+        begin += d;
+        if (d < 0) at.unit = 0;
+        if (d > 0) at = find_unit<RT, KT>(p, sums, groups, r, one, min(begin, total - 1));
+        if (c + 1 < ctas) end += moved(find_unit<RT, KT>(p, sums, groups, r, one, end));
       }
       if (lane == 0) {
         s->base = each;
         s->begin = begin;
         s->rem = rem;
-        s->count = static_cast<int>(min(end - begin, 0x7fffffffLL));
-        s->b = 32 * g + k;
-        s->h = h;
-        s->rt = rt;
-        s->unit = static_cast<int>(left);
+        s->snap = snap;
+        s->count = static_cast<int>(max(0LL, min(end - begin, 0x7fffffffLL)));
+        s->b = at.b;
+        s->h = at.h;
+        s->rt = at.rt;
+        s->unit = at.unit;
       }
     }
   }
   __syncthreads();
 }
 
+// The CTAs c0 .. c1 that an item of `units` units from unit number `item` is cut between.
+__device__ __forceinline__ void item_parts(const Share& s, long long item, int units, int& c0, int& c1) {
+  c0 = share_of(s.base, s.rem, item + s.snap);
+  c1 = max(c0, share_of(s.base, s.rem, item + max(0, units - 1 - s.snap)));
+}
+
 // ------------------------------------------------------------- split items ---
-// An item cut between CTAs c0 .. c1 leaves a partial result per CTA: in slot 2c of
-// CTA c if the item is the first of c's share, in slot 2c + 1 otherwise (it is then
-// its last).  Counter word c0 counts arrivals.  The words need no initial value: one
+// An item cut between CTAs c0 .. c1 leaves a partial result per CTA: its first part in
+// slot 2 c0 + 1 (it is the last of c0's share), the others in slot 2c of theirs.  Counter word c0 counts arrivals.  The words need no initial value: one
 // that does not carry the launch's 48-bit nonce counts as zero, and the last CTA
 // to arrive leaves zero behind, so a graph that replays the launch starts from
 // zero too.  Sums are taken in the order of the CTAs, whoever arrives last.
