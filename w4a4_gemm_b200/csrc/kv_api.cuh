@@ -37,8 +37,9 @@ bool dec_wide(const svdq_kv_attention_desc* d, int nb, int sms) {
   return tiles * d->cache.kv_heads <= sms;
 }
 
-// The tcgen05 kernel takes the call where a key head has more than this many query rows per request.
-constexpr int kRowsFrom = 32;
+// The tcgen05 kernel takes the call where a key head has more than this many query rows per request on average: its
+// tiles have 256 rows.  16 requests over 8192 keys, 8 key heads: at 24 rows 64 us against 101, at 48 rows 96 against 98.
+constexpr int kRowsFrom = 48;
 bool many_rows(const svdq_kv_attention_desc* d) {
   return d->batch > 0 && static_cast<long long>(d->rows) * (d->q_heads / d->cache.kv_heads) > static_cast<long long>(kRowsFrom) * d->batch;
 }
