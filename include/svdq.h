@@ -392,7 +392,10 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
  * window > 0 only those past position - window.  A query that sees no key gives
  * out = 0 and lse = -inf.  q_heads is a multiple of kv_heads; query head h reads
  * key head h / (q_heads / kv_heads).  Products, softmax and sums are fp32; the
- * weights exp(s - max) are rounded to fp16 for the product with the values.
+ * weights exp(s - max) are rounded to fp16 for the product with the values, as are
+ * INT4 values where a key head has many query rows per request.  `out` must not
+ * overlap q (the same pointer is refused).  The results do not depend on timing:
+ * the same call gives the same bits.
  * Rows outside cu_q[0] .. cu_q[batch] - 1 are left as they are.  What the cache holds past
  * kv_lens[b] is never used, whatever its bytes.  Out of range (bit 3): cu_q is
  * clamped to 0 .. rows, kv_lens to what the table row holds (and 2^30 - 65536), and the keys of a page

@@ -85,12 +85,12 @@ def test_refused_norms(S):
 
 def test_refused_attentions(S):
     names = [f[0] for f in S._KvAttentionDesc._fields_]
-    good = dict(cache=cache(S), q=FAKE, q_stride=256, out=FAKE, out_stride=256, lse=FAKE, cu_q=FAKE, kv_lens=FAKE, block_table=FAKE,
+    good = dict(cache=cache(S), q=FAKE, q_stride=256, out=2 * FAKE, out_stride=256, lse=FAKE, cu_q=FAKE, kv_lens=FAKE, block_table=FAKE,
                 table_stride=4, table_width=4, batch=2, rows=5, q_heads=4, causal=1, window=0, scale=0.1, workspace=FAKE)
     call = lambda **kw: S.lib().svdq_kv_attention(ctypes.byref(S._KvAttentionDesc(*[{**good, **kw}[n] for n in names])), None)  # noqa: E731
     for bad in (dict(q=None), dict(q=0x1008), dict(q_stride=252), dict(out=None), dict(out_stride=248), dict(cu_q=None), dict(kv_lens=None),
                 dict(block_table=None), dict(table_stride=3), dict(batch=-1), dict(rows=-1), dict(window=-1), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(cache=cache(S, pool=None)), dict(workspace=None), dict(workspace=0x1080), dict(cache=cache(S, fmt=3)), dict(table_width=-1)):
+                dict(scale=float("inf")), dict(cache=cache(S, pool=None)), dict(workspace=None), dict(workspace=0x1080), dict(out=FAKE), dict(cache=cache(S, fmt=3)), dict(table_width=-1)):
         assert call(**bad) == 1, bad
     for bad in (dict(q_heads=3), dict(q_heads=0), dict(batch=65537), dict(cache=cache(S, dim=32)), dict(cache=cache(S, page=20))):
         assert call(**bad) == 2, bad

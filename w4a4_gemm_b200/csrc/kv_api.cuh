@@ -343,7 +343,7 @@ SVDQ_API int svdq_kv_attention(const svdq_kv_attention_desc* d, void* stream) {
   if (d->q_heads < 1 || d->q_heads % p.g.heads != 0 || d->q_heads > 65536) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!(d->scale == d->scale) || std::isinf(d->scale)) return SVDQ_ERR_INVALID_ARG;
   if (d->rows == 0 || d->batch == 0) return SVDQ_OK;
-  if (!rows_ok(d->q, d->q_stride) || !rows_ok(d->out, d->out_stride) || d->cu_q == nullptr || d->kv_lens == nullptr ||
+  if (!rows_ok(d->q, d->q_stride) || !rows_ok(d->out, d->out_stride) || d->out == d->q || d->cu_q == nullptr || d->kv_lens == nullptr ||
       (d->table_width > 0 && d->block_table == nullptr) ||
       (d->rows > 1 && d->out_stride < static_cast<long long>(d->q_heads) * p.g.D))
     return SVDQ_ERR_INVALID_ARG;

@@ -36,6 +36,7 @@
 #include <cstdint>
 
 #include "kv_cache.cuh"
+#include "kv_common.cuh"
 #include "kv_sched.cuh"
 #include "svdq_ptx.cuh"
 

@@ -29,6 +29,7 @@
 
 #include "kv_attn.cuh"
 #include "kv_cache.cuh"
+#include "kv_common.cuh"
 #include "kv_sched.cuh"
 #include "svdq_formats.cuh"
 #include "svdq_ptx.cuh"

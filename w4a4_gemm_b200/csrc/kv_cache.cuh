@@ -16,6 +16,7 @@
 
 #include <cstdint>
 
+#include "kv_common.cuh"
 #include "svdq_formats.cuh"
 #include "svdq_ptx.cuh"
 

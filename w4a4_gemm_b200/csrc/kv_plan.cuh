@@ -18,6 +18,7 @@
 
 #include <cstdint>
 
+#include "kv_common.cuh"
 #include "svdq_ptx.cuh"
 
 namespace svdq {

@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "kv_cache.cuh"
+#include "kv_common.cuh"
 #include "svdq_ptx.cuh"
 
 namespace svdq {

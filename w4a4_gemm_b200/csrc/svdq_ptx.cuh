@@ -14,14 +14,11 @@
 namespace svdq {
 
 // ---------------------------------------------------------------- errors ---
-// Sticky device error word (bit set = a bounded wait ran out in that kernel, or
-// a cache operator skipped an index out of range).
+// Sticky device error word (bit set = a bounded wait ran out in that kernel).
 enum : unsigned {
   kErrWaitQuant = 1u << 0,
   kErrWaitGemm = 1u << 1,
   kErrWaitOther = 1u << 2,
-  kErrIndex = 1u << 3,
-  kErrWaitAttn = 1u << 4,
 };
 __device__ unsigned int g_error_word = 0;
 
