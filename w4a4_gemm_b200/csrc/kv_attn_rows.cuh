@@ -11,6 +11,13 @@
 // tiles, one issues the MMAs.  While a half's softmax runs, the tensor core works
 // for the other half.
 //
+// 4608 tokens of 24 heads attending to each other, NVFP4: 255 to 270 us, 970 to 1020
+// TFLOP/s; 3 prompts of up to 1500 tokens over up to 6000 keys, FP4 g32: 196 us, 690
+// TFLOP/s; INT4, with its second product for the keys: 561 us and 317 us.  A tile of 128
+// keys takes 3700 cycles, 2048 of them on the tensor core; the chain scores - softmax -
+// values - scores of a half (2000 + 1100 + hand-offs) bounds it, and 13 to 20 thousand
+// cycles at each end of an item.
+//
 // Numbers.  FP4 values (code * scale) are exact in fp16.  INT4 values need up to 14
 // bits: keys enter as a pair hi + lo of fp16 values (exact to 2^-22, two MMAs),
 // values are rounded once to fp16 (2^-11, below the weights' own rounding); both are

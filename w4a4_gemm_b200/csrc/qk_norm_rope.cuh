@@ -12,6 +12,9 @@
 // shuffles, and the half-split partner of an element sits in another lane at the
 // same place.  A lane group keeps its cosines, sines and weights in registers
 // over the heads of a row that it walks.
+// HBM bounds it at many rows (2 bytes in and out per element): 16383 rows of 40 heads
+// of 128, 69 us, 4.9 TB/s; 4608 rows of 48 heads, 21.7 us, 5.3 TB/s; the launch at
+// few: 16 rows 2.0 us.
 #pragma once
 
 #include <cuda_bf16.h>
