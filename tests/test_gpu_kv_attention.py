@@ -250,6 +250,14 @@ def test_attention_scores_far_apart(S, fmt):
     attend(S, R.Batch(fmt, 64, 32, 8, 2, [(2, 300)], seed=7), scale=0.0)
 
 
+@pytest.mark.parametrize("D,lens", [(128, (200, 200)), (64, (130, 400)), (128, (2, 200))])
+def test_attention_int4_small_keys_beside_large_ones(S, D, lens):
+    """From key 100 on 2^17 times larger: a causal row before it sees only the small ones, in the same tiles."""
+    size = torch.ones(lens[1], 1, 1) * 2.0 ** -6
+    size[100:] = 2.0 ** 11
+    attend(S, R.Batch("int4", D, 16, 4, 2, [lens], seed=13, k_scale=size), scale=D ** -0.5 * 2.0 ** 6)
+
+
 def test_attention_large_queries(S):
     """Queries across the range of bf16: 2^-60 to 2^60 with scales that bring the scores back."""
     for e in (-60, -20, 20, 60):

@@ -11,18 +11,20 @@
 // tiles, one issues the MMAs.  While a half's softmax runs, the tensor core works
 // for the other half.
 //
-// 4608 tokens of 24 heads attending to each other, NVFP4: 255 to 270 us, 970 to 1020
-// TFLOP/s; 3 prompts of up to 1500 tokens over up to 6000 keys, FP4 g32: 196 us, 690
-// TFLOP/s; INT4, with its second product for the keys: 561 us and 317 us.  A tile of 128
-// keys takes 3700 cycles, 2048 of them on the tensor core; the chain scores - softmax -
+// 4608 tokens of 24 heads attending to each other, NVFP4: 240 us, 1090 TFLOP/s; 3
+// prompts of up to 1500 tokens over up to 6000 keys, FP4 g32: 195 us, 690 TFLOP/s;
+// INT4, with its second product for the keys: 350 us and 232 us (561 and 317 with its
+// tiles worked out in fp32 instead of fp16 pairs).  A tile of 128 keys takes 3700 cycles,
+// 2048 of them on the tensor core; the chain scores - softmax -
 // values - scores of a half (2000 + 1100 + hand-offs) bounds it, and 13 to 20 thousand
 // cycles at each end of an item.
 //
 // Numbers.  FP4 values (code * scale) are exact in fp16.  INT4 values need up to 14
-// bits: keys enter as a pair hi + lo of fp16 values (exact to 2^-22, two MMAs),
-// values are rounded once to fp16 (2^-11, below the weights' own rounding); both are
-// divided by a power of two (the tile's largest key scale, the largest value scale so
-// far), which goes into the scores' factor and the sums' scale.  Queries are divided
+// bits: keys enter as a pair hi + lo of fp16 values (two MMAs), values are rounded once
+// to fp16 (2^-11, as the weights); both are multiplied by a power of two that brings
+// the largest scale (of the tile's keys, of the values so far) to 2^10 .. 2^11, so
+// that what fp16 keeps reaches down to scales 2^-24 of it: keys are exact to there.
+// The power goes into the scores' factor and the sums' scale.  Queries are divided
 // by a power of two per row, as in the decode kernel.  The maximum is followed
 // lazily: it moves when a row's scores pass it by more than 2^5, so most tiles leave O
 // alone; weights are exp2(x - m + 10) <= 2^15 and keep 2^-11 relative down to
@@ -48,6 +50,7 @@ constexpr int kRowsTile = 256;
 constexpr int kRowsKeys = 128;
 constexpr int kRowsRing = 4;                        // tiles whose masks and exponents are kept
 constexpr float kRowsLazy = 5.f, kRowsShift = 10.f;
+constexpr int kRowsInt4Up = 10;                     // INT4: the largest scale is brought to 2^10 .. 2^11 (times 8: below 2^14)
 
 // Shared memory: Q (two halves), K stages (hi, and lo for INT4), V stages.
 template <int FMT, int D>
@@ -566,24 +569,28 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         }
       }
     };
-    // INT4: code * scale / 2^e, rounded to fp16, and what the rounding left (LO)
-    auto int4_tile = [&](uint32_t addr, uint32_t addr_lo, const uint4 (&codes)[CW], const uint2& sc, float down, bool lo) {
+    // INT4: code * scale * 2^e, rounded to fp16, and what the rounding left (LO; exact by the fused multiply-add)
+    auto int4_tile = [&](uint32_t addr, uint32_t addr_lo, const uint4 (&codes)[CW], const uint2& sc, float up, bool lo) {
+      uint32_t s2[D / 64];
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) {
+        const float s = int4_scale(sc.x, g) * up;
+        s2[g] = pack_f16x2(s, s);
+      }
 #pragma unroll
       for (int i = 0; i < CW; ++i) {
         const uint32_t u[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = 4 * i + k;
-          const uint16_t bits = static_cast<uint16_t>(c < 8 ? sc.x & 0xffffu : sc.x >> 16);
-          const float s = __half2float(__ushort_as_half(bits)) * down;
-          uint32_t hi[4], rest[4];
+          uint32_t h[4], hi[4], rest[4];
+          int4x8_to_f16(u[k], h);                     // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+          const uint32_t v[4] = {__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410), __byte_perm(h[0], h[1], 0x7632),
+                                 __byte_perm(h[2], h[3], 0x7632)};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float a = static_cast<float>(static_cast<int>(u[k] << (28 - 8 * x)) >> 28) * s;
-            const float b = static_cast<float>(static_cast<int>(u[k] << (24 - 8 * x)) >> 28) * s;
-            hi[x] = pack_f16x2(a, b);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[x]));
-            rest[x] = pack_f16x2(a - back.x, b - back.y);
+            hi[x] = hmul2_u(v[x], s2[c / 8]);
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(rest[x]) : "r"(v[x]), "r"(s2[c / 8]), "r"(hi[x] ^ 0x80008000u));
           }
           sts128(addr + tile_chunk(key, c), hi[0], hi[1], hi[2], hi[3]);
           if (lo) sts128(addr_lo + tile_chunk(key, c), rest[0], rest[1], rest[2], rest[3]);
@@ -646,10 +653,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       if (lane == 0) masks[4 * (tile % kRowsRing) + warp - 8] = good;
       if constexpr (FMT == kFmtInt4) {
         if (threadIdx.x == 256) {
-          kexp[tile % kRowsRing] = ek;
-          vexp[tile % kRowsRing] = run_ev;
+          kexp[tile % kRowsRing] = ek - kRowsInt4Up;
+          vexp[tile % kRowsRing] = run_ev - kRowsInt4Up;
         }
-        int4_tile(kaddr, kaddr + L::kTile, k.c, k.s, pow2(-ek), true);
+        int4_tile(kaddr, kaddr + L::kTile, k.c, k.s, pow2(kRowsInt4Up - ek), true);
       } else {
         fp4_tile(kaddr, k.c, k.s);
       }
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       k = fetch(next_at, page_next, next_h, false);
       if (!wait(&v_empty[vs], ((tile / L::kVStages) & 1) ^ 1)) break;
       if constexpr (FMT == kFmtInt4)
-        int4_tile(vaddr, 0u, v.c, v.s, pow2(-run_ev), false);
+        int4_tile(vaddr, 0u, v.c, v.s, pow2(kRowsInt4Up - run_ev), false);
       else
         fp4_tile(vaddr, v.c, v.s);
       fence_proxy_async_smem();
