@@ -372,7 +372,9 @@ SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* desc, void* stream)
 /* Quantize the keys and values of M rows (bf16 M x kv_heads x head_dim, strides
  * in elements) into their slots.  A row with a slot below 0 is skipped, as is
  * (bit 3) one past the pool.  The slots >= 0 of a call must differ; what two
- * rows leave in the same slot is unspecified.  The values must be finite. */
+ * rows leave in the same slot is unspecified.  What is held is always finite: an
+ * infinity counts as the format's largest value (6 x 448, or 7 x 65504), a group
+ * of NaN alone as zeros, a NaN beside numbers as some value of its group's scale. */
 SVDQ_API int svdq_kv_append(const svdq_kv_cache* cache, const void* k, const void* v, long long k_stride,
                             long long v_stride, const int64_t* slots, int M, void* stream);
 

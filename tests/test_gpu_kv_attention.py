@@ -204,6 +204,31 @@ def strip(pool, fmt, D, page):
     return out
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens", [(3, 100), (100, 100)])
+def test_append_of_what_is_not_finite(S, fmt, lens):
+    """A token with infinities and NaN is held by finite values, and rows that mask it do not see it."""
+    b = R.Batch(fmt, 128, 16, 4, 2, [lens], seed=14)
+    c, n, kv = cache_of(S, b), *lens
+    bad = torch.randn(1, 4, 128, generator=torch.Generator().manual_seed(1))
+    bad[0, :, 7], bad[0, :, 40], bad[0, :, 90] = float("inf"), float("-inf"), float("nan")
+    bad[0, 1] = float("nan")
+    bad[0, 3] = float("inf")
+    bad = bad.to(torch.bfloat16).cuda()
+    slot = int(b.table[0, (kv - 1) // 16]) * 16 + (kv - 1) % 16
+    S.svdq_kv_append(c, bad[:, :2], bad[:, 2:], dev([slot], torch.int64))
+    k, v = S.svdq_kv_read(c, dev([slot], torch.int64), torch.float32)
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+    most = 7 * 65504 if fmt == "int4" else 6 * 448
+    assert (v[0, 1] == most).all() and (k[0, 1] == 0).all()
+    assert (k[0, 0, 7], k[0, 0, 40], v[0, 0, 7], v[0, 0, 40]) == (most, -most, most, -most)
+    b.keys[0][-1], b.values[0][-1] = k[0].double().cpu(), v[0].double().cpu()
+    out, lse = S.svdq_kv_attention(c, b.q.cuda(), dev(b.cu), dev([kv], torch.int32), dev(b.table), return_lse=True)
+    o, l, to, tl = b.expected(128 ** -0.5, True, 0)
+    within(out[:n - 1], o[:n - 1], to[:n - 1])
+    within(lse[:n - 1], l[:n - 1], tl[:n - 1])
+
+
 def test_append_and_read_past_the_pool(S):
     c = S.KVCache("nvfp4", 2, 64, 16, torch.zeros(3, 2, 2 * 16 * 36, dtype=torch.uint8, device="cuda"))
     k = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")

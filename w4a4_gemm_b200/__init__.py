@@ -491,7 +491,7 @@ def svdq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, table: Optional[torch.Te
 
 def svdq_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
     """Quantize k and v (bf16 rows x kv_heads x head_dim) into the cache at `slots` (int64 rows;
-    below 0: a padded row, skipped)."""
+    below 0: a padded row, skipped).  An infinity is held as the format's largest value."""
     r = (_fast or _ext()).kv_append(cache._c, k, v, slots, _handle(stream))
     if type(r) is int:
         _check(r, "svdq_kv_append")

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     float x[8];
     bf16x8_to_floats(raw[u], x);
     float amax = fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
-    amax = fmaxf(amax, 0.f);
+    amax = fminf(fmaxf(amax, 0.f), 3.402823466e+38f);  // not infinite: a NaN scale would reach rows that mask the key
     constexpr int kLanes = kv_group(FMT) / 8;          // lanes that share a scale
 #pragma unroll
     for (int o = 1; o < kLanes; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
