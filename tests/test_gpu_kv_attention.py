@@ -447,6 +447,20 @@ def test_attention_split_items(S, fmt, D, hq, hk, lens):
     attend(S, b, window=300)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_ends_of_items(S, fmt, D):
+    """Full tiles of 256 rows followed by tiles of 1 to 32, several of each per CTA: the warps of a half that have
+    no row of the next item start on it at once, while the others still write the last one's rows.  Every
+    row is right, and every call gives the same bits."""
+    b = R.Batch(fmt, D, 16, 8, 8, [(257 + i % 32, 257 + i % 32 + 37 * (i % 7)) for i in range(40)], seed=50)
+    out, lse = attend(S, b)
+    args = (cache_of(S, b), b.q.cuda(), dev(b.cu), dev([kv for _, kv in b.lens], torch.int32), dev(b.table))
+    for _ in range(30):
+        again = S.svdq_kv_attention(*args, return_lse=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_attention_many_requests(S):
     """More requests than a scan's first level, most of them without new tokens."""
     rng = np.random.default_rng(5)

@@ -393,10 +393,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       float unscale = 1.f;
       if constexpr (FMT == kFmtInt4) unscale = pow2(ev);
       // The finished rows leave through the half's query tile (its MMAs are done): a lane writes its row as
-      // 16-byte chunks, swizzled, and the warp copies its 32 rows out D / 8 lanes a row.
-      const uint32_t stage = q_addr + (warp & 3) * 32 * (D * 2);
+      // 16-byte chunks, and the warp copies its 32 rows out D / 8 lanes a row.  A row lies where its query lay: the
+      // warps of a half do not wait for each other here, and a warp whose next queries are already in the tile must
+      // find no other warp's rows in its own, nor leave its rows in theirs.
       auto put = [&](int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        sts128(stage + lane * (D * 2) + ((chunk ^ (lane & 7)) << 4), a, b, c, d);
+        sts128(q_addr + tile_chunk((warp & 3) * 32 + lane, chunk), a, b, c, d);
       };
       auto copy_out = [&]() {
         __syncwarp();
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           const int gr = w.rt * RT + half * 128 + (warp & 3) * 32 + lr;
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage + lr * (D * 2) + ((c ^ (lr & 7)) << 4)) : "memory");
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(q_addr + tile_chunk((warp & 3) * 32 + lr, c)) : "memory");
           if (gr < rows) {
             const int tk = gr / p.rep;
             *reinterpret_cast<uint4*>(p.out + (w.req.row0 + tk) * p.out_stride + (w.h * p.rep.d + (gr - tk * p.rep.d)) * D + 8 * c) = v;
