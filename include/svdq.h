@@ -399,7 +399,9 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
  * overlap q (the same pointer is refused).  The results do not depend on timing:
  * the same call gives the same bits.
  * Rows outside cu_q[0] .. cu_q[batch] - 1 are left as they are.  What the cache holds past
- * kv_lens[b] is never used, whatever its bytes.  Out of range (bit 3): cu_q is
+ * kv_lens[b], or in front of the window of the request's first query, is never used, whatever
+ * its bytes, and the entries of whole pages there are not looked at (a page that the window has
+ * left can be freed).  Out of range (bit 3): cu_q is
  * clamped to 0 .. rows, kv_lens to what the table row holds (and 2^30 - 65536), and the keys of a page
  * outside the pool are masked.  `workspace` (svdq_kv_attention_workspace_bytes,
  * 256-byte aligned, no initial contents) is scratch of this call: calls that may

@@ -258,6 +258,35 @@ def test_attention_masks(S, causal, window, D, hq, hk, lens):
     attend(S, R.Batch("nvfp4", D, 16, hq, hk, lens, seed=3), causal=causal, window=window)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,page,causal,window,lens", [
+    (128, 16, True, 70, [(1, 900), (2, 333)]), (64, 64, True, 1, [(1, 700), (1, 65)]), (128, 128, False, 33, [(4, 1000)]),
+    (64, 32, True, 200, [(1, 3000)]), (128, 16, True, 40, [(150, 900), (100, 333)]), (64, 64, True, 1, [(300, 700)]),
+    (128, 256, False, 33, [(70, 1000)])])
+def test_attention_in_front_of_the_window(S, fmt, D, page, causal, window, lens):
+    """Pages that lie in front of every query's window may be gone (-1) or hold anything, and so may the tokens
+    in front of it in its first page: infinite and NaN scales there reach nothing, and no bit is set."""
+    b = R.Batch(fmt, D, page, 8, 2, lens, seed=60)
+    ks, vc, vs, end = R.pieces(fmt, D, page)
+    gone = b.table.copy()
+    spare = (set(range(b.pool.shape[0])) - set(b.table.reshape(-1).tolist())).pop()
+    other = b.table.copy()
+    for r, (n, kv) in enumerate(lens):
+        low = max(0, kv - n - window + 1)             # the first query's first key
+        gone[r, :low // page] = -1
+        other[r, :low // page] = spare
+        p, o = b.table[r, low // page], low % page
+        for c0, s0, s1 in ((0, ks, vc), (vc, vs, end)):
+            w = (s1 - s0) // page
+            b.pool[p, :, c0:c0 + o * D // 2] = 0x5A
+            b.pool[p, :, s0:s0 + o * w] = 0x7F if fmt != "int4" else np.tile(np.array([0x00, 0x7C], np.uint8), o * w // 2)
+    for byte in (0x7F, 0x7C, 0xFF):                   # NaN; fp16 NaN and E4M3 384; NaN
+        b.pool[spare] = byte
+        for t in (gone, other):
+            b.table = t
+            attend(S, b, causal=causal, window=window)
+
+
 @pytest.mark.parametrize("lens", [[(5, 3)], [(200, 70), (1, 0), (3, 0)], [(1, 0)], [(0, 0), (0, 9)]])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_rows_without_keys(S, lens, causal):

@@ -275,14 +275,14 @@ __device__ __forceinline__ void key_scores(const uint8_t* codes, const uint8_t* 
 }
 
 // O^T += V^T P^T for 16 keys.  w[nb][0..3]: the weights of this lane's score elements (keys of rows r and
-// r + 8, columns 2t and 2t + 1).  `usable`: keys below it are real, scales of the others count as zero (FP4).
+// r + 8, columns 2t and 2t + 1).  Scales of keys outside `from` .. `usable` - 1 count as zero (FP4).
 // INT4: `sc` holds the fp16 scales of the keys of rows r and r + 8, `down` the power of two that they are
 // divided by.
 __device__ __forceinline__ float int4_scale(uint32_t two, int g) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(g ? two >> 16 : two & 0xffffu)));
 }
 template <int FMT, int D, int NB, bool WHOLE>
-__device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* scales, int r, int t, int usable, const uint32_t (&sc)[2],
+__device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* scales, int r, int t, int from, int usable, const uint32_t (&sc)[2],
                                            float down, const float (&w)[NB][4], float (&o)[NB][D / 16][4]) {
   int key[4];                                         // keys of contraction indices 2t, 2t + 1, 2t + 8, 2t + 9
   key[0] = t, key[1] = 4 + (t ^ 1), key[2] = 8 + t, key[3] = 12 + (t ^ 1);
@@ -334,7 +334,7 @@ __device__ __forceinline__ void add_values(const uint8_t* codes, const uint8_t* 
       } else {
         c[i][0] = *reinterpret_cast<const uint32_t*>(at);
       }
-      sc[i] = WHOLE || key[i] < usable ? scales[key[i] * SB + g] : 0u;
+      sc[i] = WHOLE || (key[i] >= from && key[i] < usable) ? scales[key[i] * SB + g] : 0u;
     }
     const uint32_t s01 = e4m3x2_to_f16(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16(sc[2] | (sc[3] << 8));
 #pragma unroll
@@ -366,9 +366,9 @@ __device__ __forceinline__ int value_element(int r, int j) {
 }
 
 // Weights and values of one step: kDecBlocks blocks of 16 keys from `kc`.  WHOLE: every row sees every key.
-// `base` is the first key, `have` a bit per block that was loaded.
+// `base` is the first key, `have` a bit per block that was loaded, `low` .. `limit` - 1 the keys that count.
 template <int FMT, int D, int NB, bool WHOLE>
-__device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int base, int have, int limit, const uint32_t (&qf)[NB][D / 8],
+__device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int base, int have, int low, int limit, const uint32_t (&qf)[NB][D / 8],
                                          const float (&factor)[NB][2], const int (&lo_key)[NB][2], const int (&hi_key)[NB][2],
                                          float (&m)[NB][2], float (&l)[NB][2], float (&o)[NB][D / 16][4], int& vexp) {
   constexpr int SB = kv_scale_bytes(FMT, D);
@@ -387,7 +387,8 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
       for (int k = 0; k < 2; ++k) {
         const uint8_t* at = vs + (16 * u + kr + 8 * k) * SB;
         uint32_t two = D == 128 ? *reinterpret_cast<const uint32_t*>(at) : *reinterpret_cast<const uint16_t*>(at);
-        if (!WHOLE && (!((have >> u) & 1) || base + 16 * u + kr + 8 * k >= limit)) two = 0u;
+        const int key = base + 16 * u + kr + 8 * k;
+        if (!WHOLE && (!((have >> u) & 1) || key < low || key >= limit)) two = 0u;
         sv[u][k] = two;
         big = __vmaxu2(big, two);                     // fp16 of one sign order like integers
       }
@@ -466,7 +467,7 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
 #pragma unroll
   for (int u = 0; u < kDecBlocks; ++u) {
     const int usable = WHOLE ? 16 : (((have >> u) & 1) ? limit - base - 16 * u : 0);
-    add_values<FMT, D, NB, WHOLE>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, usable, sv[u], down, s[u], o);
+    add_values<FMT, D, NB, WHOLE>(vc + u * 16 * (D / 2), vs + u * 16 * SB, r, t, low - base - 16 * u, usable, sv[u], down, s[u], o);
   }
 }
 
@@ -522,8 +523,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
   const bool copier = (lane << piece_log2) < kDecChunk;
 
   while (true) {
-    int k0, k1;
-    tile_keys<RT, UNIT>(p, req, rt, k0, k1);
+    int k0, k1, low;
+    tile_keys<RT, UNIT>(p, req, rt, k0, k1, low);
     const int units = max(1, (k1 - k0 + UNIT - 1) / UNIT);
     const int here = min(units - unit, count);
     const int first = k0 + unit * UNIT;           // keys of this segment
@@ -536,11 +537,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
       key += UNIT;
       return c;
     };
-    // The page of this lane's piece of the step at `next`: -1 past the end, or outside the pool.
+    // The page of this lane's piece of the step at `key0`: -1 where no row sees a key of it, or outside the pool.
     auto page_of = [&](int key0) {
       const int key = key0 + (lane << piece_log2);
       int page = -1;
-      if (copier && key0 >= 0 && key < limit) {
+      if (copier && key0 >= 0 && key < limit && key + piece > low) {
         page = table[key >> p.g.page_log2];
         if (page >= p.g.num_pages) page = -2;
         if (page < 0) raise_error(kErrIndex);
@@ -642,9 +643,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
       const uint8_t* kc = ring + st * STAGE;
       const int have = loaded[st].x, base = loaded[st].y;
       if (have == (1 << kDecBlocks) - 1 && base >= all_lo && base + kDecChunk <= all_hi)
-        dec_step<FMT, D, NB, true>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
+        dec_step<FMT, D, NB, true>(kc, r, t, base, have, low, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
       else
-        dec_step<FMT, D, NB, false>(kc, r, t, base, have, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
+        dec_step<FMT, D, NB, false>(kc, r, t, base, have, low, limit, qf, factor, lo_key, hi_key, m, l, o, vexp);
       phase ^= 1u << st;
       --flying;
       __syncwarp();                                   // every lane has left the stage

@@ -123,11 +123,11 @@ struct Walk {
   int b, h, rt, unit, count;
   long long at;                  // unit number of the segment's first unit
   Request req;
-  int k0, k1, units, here, first;
+  int k0, k1, low, units, here, first;
 };
 template <int RT, int KT>
 __device__ __forceinline__ void walk_segment(const AttnParams& p, Walk& w) {
-  tile_keys<RT, KT>(p, w.req, w.rt, w.k0, w.k1);
+  tile_keys<RT, KT>(p, w.req, w.rt, w.k0, w.k1, w.low);
   w.units = max(1, (w.k1 - w.k0 + KT - 1) / KT);
   w.here = min(w.units - w.unit, w.count);
   w.first = w.k0 + w.unit * KT;
@@ -509,14 +509,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
     Walk w = walk_start<RT, KT>(p, share);
     bool more = w.count > 0;
     // A tile's key codes are loaded while the values of the tile before are turned over, and its value codes while
-    // its keys are; its page is looked up a tile ahead.  A key past the segment or in a bad page reads as zeros.
+    // its keys are; its page is looked up a tile ahead.  A key that no row of the item sees or in a bad page reads as zeros.
     struct Raw {
       uint4 c[CW];
       uint2 s;
     };
     auto page_of = [&](const Walk& w, int j) {
       const int t = w.first + j * KT + key;
-      if (t >= w.k1) return -1;
+      if (t >= w.k1 || t < w.low) return -1;
       const int page = p.table[w.b * p.table_stride + (t >> p.g.page_log2)];
       if (page < 0 || page >= p.g.num_pages) {
         raise_error(kErrIndex);

@@ -80,20 +80,21 @@ __device__ __forceinline__ Request load_request(const AttnParams& p, int b) {
   return r;
 }
 
-// Keys [k0, k1) that any row of tile rt sees; k0 is cut down to a multiple of KT.
+// Keys [low, k1) that any row of tile rt sees; k0 is low cut down to a multiple of KT.  What lies between k0 and low
+// is in front of every row's window: its pages may be gone and its bytes anything, so it is neither looked up nor used.
 template <int RT, int KT>
-__device__ __forceinline__ void tile_keys(const AttnParams& p, const Request& r, int rt, int& k0, int& k1) {
+__device__ __forceinline__ void tile_keys(const AttnParams& p, const Request& r, int rt, int& k0, int& k1, int& low) {
   const int rows = r.n * p.rep.d;
   k1 = p.causal ? max(0, min(r.kv, r.kv - r.n + (min((rt + 1) * RT, rows) - 1) / p.rep + 1)) : r.kv;
-  k0 = p.window > 0 ? max(0, r.kv - r.n + (rt * RT) / p.rep - p.window + 1) : 0;
-  k0 = min(k0, k1) / KT * KT;
+  low = min(k1, p.window > 0 ? max(0, r.kv - r.n + (rt * RT) / p.rep - p.window + 1) : 0);
+  k0 = low / KT * KT;
 }
 
 // Units of a tile: at least one, so that rows without keys are written too.
 template <int RT, int KT>
 __device__ __forceinline__ int tile_units(const AttnParams& p, const Request& r, int rt) {
-  int k0, k1;
-  tile_keys<RT, KT>(p, r, rt, k0, k1);
+  int k0, k1, low;
+  tile_keys<RT, KT>(p, r, rt, k0, k1, low);
   return max(1, (k1 - k0 + KT - 1) / KT);
 }
 
