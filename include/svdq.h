@@ -392,7 +392,8 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
  * block_table[b][t / page_size].  Query i of n sits at position
  * kv_lens[b] - n + i; with `causal` it sees keys up to its own position, with
  * window > 0 only those past position - window.  A query that sees no key gives
- * out = 0 and lse = -inf.  q_heads is a multiple of kv_heads; query head h reads
+ * out = 0 and lse = -inf; one with a NaN or an infinity gives what the formula gives, NaN
+ * as a rule, in both.  q_heads is a multiple of kv_heads; query head h reads
  * key head h / (q_heads / kv_heads).  Products, softmax and sums are fp32; the
  * weights exp(s - max) are rounded to fp16 for the product with the values, as are
  * INT4 values where a key head has many query rows per request.  `out` must not

@@ -320,6 +320,27 @@ def test_attention_large_queries(S):
         attend(S, b, scale=128 ** -0.5 * 2.0 ** -e)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens", [[(1, 300), (2, 90)], [(1, 9000)], [(150, 300)], [(500, 2500)]])
+def test_attention_queries_that_are_not_finite(S, fmt, lens):
+    """A query with a NaN or an infinity gives NaN in its output and in its lse (-inf says that a query sees no
+    key), whole or joined from parts, and the other rows and heads of its tile do not see it."""
+    b = R.Batch(fmt, 64, 64, 6, 2, lens, seed=70)
+    q = b.q.clone()
+    bad = torch.zeros(b.rows, 6, dtype=torch.bool)
+    for row, head, at, x in ((0, 0, 5, "nan"), (0, 4, slice(None), "nan"), (-1, 1, 7, "inf"), (-1, 5, slice(None), "-inf")):
+        q[row, head, at] = float(x)
+        bad[row, head] = True
+    out, lse = S.svdq_kv_attention(cache_of(S, b), q.cuda(), dev(b.cu), dev([kv for _, kv in lens], torch.int32), dev(b.table),
+                                   return_lse=True)
+    assert out.cpu()[bad].isnan().all() and lse.cpu()[bad].isnan().all()
+    o, l, to, tl = b.expected(64 ** -0.5, True, 0)
+    fine = ~bad.numpy()
+    within(out[~bad.cuda()], o[fine], to[fine])
+    within(lse[~bad.cuda()], l[fine], tl[fine])
+    assert S.svdq_get_error() == 0
+
+
 @pytest.mark.parametrize("lens", [[(1, 300), (1, 40)], [(150, 300), (20, 40)]])
 def test_attention_strided_padded_and_repeated(S, lens):
     """Queries as a view of wider rows, an output of its own stride with padded rows and

@@ -471,15 +471,15 @@ __device__ __forceinline__ void dec_step(const uint8_t* kc, int r, int t, int ba
   }
 }
 
-// Writes four elements of a finished row, and its lse.
+// Writes four elements of a finished row, and its lse.  A sum of 0 is a row without keys; one that is NaN stays NaN.
 template <int FMT>
 __device__ __forceinline__ void write_row(const AttnParams& p, int row0, int h, int row, int d, int D, float4 acc, float top, float sum) {
   const int i = row / p.rep, hq = h * p.rep.d + row - i * p.rep.d;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<uint2*>(p.out + (row0 + i) * p.out_stride + hq * D + d) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (p.lse != nullptr && d == 0)
-    p.lse[static_cast<long long>(row0 + i) * p.q_heads + hq] = sum > 0.f ? (top - dec_shift(FMT) + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    p.lse[static_cast<long long>(row0 + i) * p.q_heads + hq] = sum == 0.f ? -INFINITY : (top - dec_shift(FMT) + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int FMT, int D, int NB, int WARPS>
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kDecWide ? 1 : 3) kv_attn
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
         const float mw = row_max[w * RT + row];
-        sum += mw == -INFINITY ? 0.f : row_sum[w * RT + row] * ex2(mw - top);
+        sum += row_sum[w * RT + row] * (mw == -INFINITY ? 0.f : ex2(mw - top));
         const float4 v = *reinterpret_cast<const float4*>(all + w * kWarpFloats + row * PITCH + d);
         acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
       }

@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       // a partial result: [D / 4][256] float4, so that the lanes of a store are neighbours; then [256] (max, sum)
       float4* slot = reinterpret_cast<float4*>(p.partials + (2ll * blockIdx.x + (w.unit == 0 ? 1 : 0)) * SLOT);
       const int srow = half * 128 + lrow;
-      const float inv = l > 0.f ? unscale / l : 0.f;
+      const float inv = l == 0.f ? 0.f : unscale / l;    // a row without keys; a sum that is NaN stays NaN
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
       float* lse = p.lse == nullptr || !live ? nullptr : p.lse + static_cast<long long>(w.req.row0 + tok) * p.q_heads + hq;
       if (!split) {
         copy_out();
-        if (lse != nullptr) *lse = l > 0.f ? (m - kRowsShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (lse != nullptr) *lse = l == 0.f ? -INFINITY : (m - kRowsShift + log2f(l)) * 0.6931471805599453f;
       } else {
         __stcg(reinterpret_cast<float2*>(slot + RT * (D / 4)) + srow, make_float2(m, l));
         // each half of an item is joined by itself, by the CTA whose four warps arrive last
@@ -467,10 +467,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
           for (int c = c0; c <= c1; ++c) {
             const float2 ms = __ldcg(reinterpret_cast<const float2*>(part(c) + RT * (D / 4)) + srow);
             const float m2 = fmaxf(top, ms.x);
-            if (m2 > -INFINITY) total = total * ex2(top - m2) + ms.y * ex2(ms.x - m2);
+            total = m2 > -INFINITY ? total * ex2(top - m2) + ms.y * ex2(ms.x - m2) : total + ms.y;   // 0 or NaN
             top = m2;
           }
-          const float each = total > 0.f ? 1.f / total : 0.f;
+          const float each = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll 1
           for (int d = 0; d < D / 4; d += 8) {
             float4 acc[8];
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
                   pack_bf16x2(acc[2 * i + 1].x, acc[2 * i + 1].y), pack_bf16x2(acc[2 * i + 1].z, acc[2 * i + 1].w));
           }
           copy_out();
-          if (lse != nullptr) *lse = total > 0.f ? (top - kRowsShift + log2f(total)) * 0.6931471805599453f : -INFINITY;
+          if (lse != nullptr) *lse = total == 0.f ? -INFINITY : (top - kRowsShift + log2f(total)) * 0.6931471805599453f;
         }
       }
       more = walk_next<RT, KT>(p, w);
