@@ -511,6 +511,15 @@ def test_attention_ends_of_items(S, fmt, D):
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("hk,lens", [(46, [(700, 700)]), (18, [(1000, 1000), (1000, 1020)]), (40, [(1000, 250), (1000, 200)]),
+                                     (24, [(1000, 1000), (1000, 1200)])])
+def test_attention_items_of_one_length(S, hk, lens):
+    """Fewer equal items than CTAs, as many and more; equal keys from unequal lengths; and items that are not equal."""
+    b = R.Batch("fp4g32", 64, 32, hk, hk, lens, seed=80)
+    attend(S, b, causal=False)
+    attend(S, b, causal=False, window=400)
+
+
 def test_attention_many_requests(S):
     """More requests than a scan's first level, most of them without new tokens."""
     rng = np.random.default_rng(5)

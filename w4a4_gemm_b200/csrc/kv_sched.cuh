@@ -231,10 +231,18 @@ __device__ __forceinline__ Place find_unit(const AttnParams& p, const long long*
   return at;
 }
 
+// A cut costs the many-row kernel one more end of an item, 13 to 20 thousand cycles where a unit takes 3700.
+constexpr int kCutUnits = 5;
+
 // Called by all threads.  `sums` holds (batch + 31) / 32 words of shared memory.
-// SNAP: a boundary between shares that lies within share.snap units of an item's end moves there (a sixth of a
-// share at most: a cut costs both sides a partial result, about three units of the many-row kernel.  432 items of 36
-// units: 240 us, with an eighth 255; one request of 2500 rows over 6000 keys 166 us, with an eighth 160).
+// SNAP: a boundary between shares that lies within share.snap units of an item's end moves there: by what a cut costs,
+// kCutUnits, at most, so that no share pays more for the longer way than the cut would have cost it (and by a sixth of
+// a share, so that boundaries keep their order).  A prompt of 4096 tokens, 32 query and 8 key heads: 209 us, 227 if none
+// moves, 204 if all within a sixth of a share do; 2500 tokens over 6000 keys: 208, 209 and 235.
+// Items of one length are not cut at all where whole ones make the largest share no more than kCutUnits longer than
+// equal shares.  Tokens attending to each other, uncut and cut: 2048 of 18 heads (144 items of 16 units) 47 and 61 us;
+// 2304 of 32 heads (288 of 18) 92 and 107; 4608 of 24 heads (432 of 36) 240 and 257; but 4096 of 24 heads (384 of 32, in
+// the largest share 96, in equal ones 83) 220 and 214.
 template <int RT, int KT, bool SNAP>
 __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums, Share* s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -259,7 +267,18 @@ __device__ __forceinline__ void find_share(const AttnParams& p, long long* sums,
     } else {
       const long long each = div_units(total, ctas);
       const int rem = static_cast<int>(total - each * ctas);
-      const int snap = SNAP ? static_cast<int>(min(each / 6, 64LL)) : 0;
+      int snap = 0;
+      if (SNAP) {
+        snap = static_cast<int>(min(each / 6, static_cast<long long>(kCutUnits)));
+        if (groups == 1 && !p.causal && p.window == 0) {         // the tiles of a request are alike
+          const int len = row_tiles<RT>(p, r) > 0 ? tile_units<RT, KT>(p, r, 0) : 0;
+          const int most = __reduce_max_sync(0xffffffffu, len);
+          if (__all_sync(0xffffffffu, len == 0 || len == most)) {
+            const long long items = div_units(total, most), whole = div_units(items + ctas - 1, ctas) * most;
+            if (whole <= each + kCutUnits) snap = max(snap, most / 2);   // every boundary is as near to an end
+          }
+        }
+      }
       long long begin = share_begin(each, rem, c), end = share_begin(each, rem, c + 1);
       Place at = find_unit<RT, KT>(p, sums, groups, r, one, begin);
       if (SNAP) {
