@@ -653,3 +653,19 @@ def test_refused_tensors(S):
         S.KVCache("nvfp4", 2, 64, 16, torch.zeros(4, 2, 100, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert S.svdq_get_error() == 0
+
+
+@pytest.mark.parametrize("flag", ["norm", "interleaved", "causal", "return_lse"])
+def test_refused_truth_values(S, flag):
+    """A flag that has no truth value is a TypeError, and nothing is written."""
+    x = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, two = torch.full_like(x, 7), torch.zeros(2)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    with pytest.raises(TypeError):
+        if flag in ("norm", "interleaved"):
+            S.svdq_qk_norm_rope(x, x, q_out=out, k_out=out.clone(), **{flag: two})
+        else:
+            c = S.KVCache("nvfp4", 2, 64, 16, torch.zeros(4, 2, 1152, dtype=torch.uint8, device="cuda"))
+            S.svdq_kv_attention(c, x, i32(0, 3), i32(3), torch.zeros(1, 4, dtype=torch.int32, device="cuda"), out=out, **{flag: two})
+    torch.cuda.synchronize()
+    assert (out == 7).all()

@@ -116,7 +116,14 @@ double number(PyObject* o, const char* name) {
   }
   return v;
 }
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    bad_type(std::string(name) + " must be a truth value");
+  }
+  return v == 1;
+}
 
 // The stream that the call runs on: the caller's (a cudaStream_t as an int; outputs are then allocated for
 // it) or the current one.
@@ -245,8 +252,8 @@ PyObject* qk_norm_rope(PyObject* const* a, Py_ssize_t n) {
   if (a[4] != Py_None) d.q_weight = array(a[4], at::kBFloat16, "q_weight", dev, dim).data_ptr();
   if (a[5] != Py_None) d.k_weight = array(a[5], at::kBFloat16, "k_weight", dev, dim).data_ptr();
   d.eps = static_cast<float>(number(a[6], "eps"));
-  d.norm = truth(a[7]);
-  d.interleaved = truth(a[8]);
+  d.norm = truth(a[7], "norm");
+  d.interleaved = truth(a[8], "interleaved");
   d.rows = static_cast<int>(rows);
   d.q_heads = static_cast<int>(hq);
   d.k_heads = static_cast<int>(hk);
@@ -283,7 +290,7 @@ PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
   const int dev = here();
   const Cache& c = cache_of(a[0], dev);
   const at::Tensor& slots = array(a[1], at::kLong, "slots", dev);
-  const bool fp32 = truth(a[2]);
+  const bool fp32 = truth(a[2], "fp32");
   Launch on(a[3], dev);
   const at::ScalarType dtype = fp32 ? at::kFloat : at::kBFloat16;
   at::Tensor k = make({slots.size(0), c.c.kv_heads, c.c.head_dim}, dtype, slots.device());
@@ -332,14 +339,14 @@ PyObject* kv_attention(PyObject* const* a, Py_ssize_t n) {
   d.rows = static_cast<int>(rows);
   d.q_heads = static_cast<int>(heads);
   d.scale = a[5] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(dim))) : static_cast<float>(number(a[5], "scale"));
-  d.causal = truth(a[6]);
+  d.causal = truth(a[6], "causal");
   d.window = small(a[7], "window");
   Launch on(a[11], dev);
   at::Tensor out = a[8] == Py_None ? make({rows, heads, dim}, at::kBFloat16, q.device()) : tensor(a[8], at::kBFloat16, "out", dev);
   r = check_rows(out, "out", rows, heads, dim, true);
   d.out = r.p, d.out_stride = r.stride;
   at::Tensor lse;
-  if (truth(a[9])) {
+  if (truth(a[9], "return_lse")) {
     lse = make({rows, heads}, at::kFloat, q.device());
     d.lse = static_cast<float*>(lse.data_ptr());
   }
