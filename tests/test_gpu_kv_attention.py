@@ -608,6 +608,32 @@ def test_attention_wait_expiry_is_reported_and_recovered(S, lens):
     assert S.svdq_get_error() == 0 and torch.equal(again, want)
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "int4"])
+def test_attention_wait_expiry_of_long_items(S, fmt):
+    """Items of many tiles, whose roles wait for each other longer than the hardware holds a poll: with a budget of one
+    cycle a wait of the many-row kernel does run out (bit 4 is seen, and no other), the launch ends by itself, and
+    with the budget restored the same call gives the same bits again.  (The few-row kernel waits for nothing but its own
+    copies, which land within a poll.)"""
+    lens = [(1500, 3000)] * 3
+    b = R.Batch(fmt, 128, 64, 8, 2, lens, seed=14)
+    args = (cache_of(S, b), b.q.cuda(), dev(b.cu), dev([kv for _, kv in lens], torch.int32), dev(b.table))
+    want = S.svdq_kv_attention(*args)
+    torch.cuda.synchronize()
+    assert S.svdq_get_error() == 0
+    seen = []
+    try:
+        S.svdq_set_wait_budget(1)
+        for _ in range(20):
+            S.svdq_kv_attention(*args)
+            seen.append(S.svdq_get_error())
+    finally:
+        S.svdq_set_wait_budget(1 << 31)
+    assert set(seen) <= {0, 16} and 16 in seen, seen
+    again = S.svdq_kv_attention(*args)
+    torch.cuda.synchronize()
+    assert S.svdq_get_error() == 0 and torch.equal(again, want)
+
+
 def test_refused_tensors(S):
     """What the Python calls refuse before anything is launched."""
     c = S.KVCache("nvfp4", 2, 64, 16, num_pages=4)
