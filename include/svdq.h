@@ -323,7 +323,7 @@ SVDQ_API int svdq_kv_page_bytes(const svdq_kv_cache* cache, size_t* bytes);
  * Out of range (bit 3): a negative length or a total past 2^31 - 1 counts as no
  * new tokens; tokens past `rows` are dropped (cu_q and total_lens say so); a page
  * past table_width or past free_count is not entered (or entered as -1), its
- * tokens get slot -1.  batch <= 16384. */
+ * tokens get slot -1.  batch <= 16384, rows <= 2^30. */
 typedef struct {
   const int* q_lens;       /* batch */
   const int* kv_lens;      /* batch */
@@ -374,7 +374,8 @@ SVDQ_API int svdq_qk_norm_rope(const svdq_qk_norm_rope_desc* desc, void* stream)
  * (bit 3) one past the pool.  The slots >= 0 of a call must differ; what two
  * rows leave in the same slot is unspecified.  What is held is always finite: an
  * infinity counts as the format's largest value (6 x 448, or 7 x 65504), a group
- * of NaN alone as zeros, a NaN beside numbers as some value of its group's scale. */
+ * of NaN alone as zeros, a NaN beside numbers as some value of its group's scale.
+ * M <= 2^30, here and in svdq_kv_read. */
 SVDQ_API int svdq_kv_append(const svdq_kv_cache* cache, const void* k, const void* v, long long k_stride,
                             long long v_stride, const int64_t* slots, int M, void* stream);
 

@@ -100,6 +100,16 @@ def test_refused_attentions(S):
     assert S.lib().svdq_kv_attention_workspace_bytes(None, ctypes.byref(n)) == 1
 
 
+def test_refused_row_counts(S):
+    """Rows past 2^30 would pass 32 bits where the kernels count rows and CTAs."""
+    L, c, many = S.lib(), ctypes.byref(cache(S)), 2 ** 30 + 1
+    assert L.svdq_kv_append(c, FAKE, FAKE, 0, 0, FAKE, many, None) == 2
+    assert L.svdq_kv_read(c, FAKE, many, 0, FAKE, FAKE, None) == 2
+    names = [f[0] for f in S._KvPlanDesc._fields_]
+    plan = dict.fromkeys(names, FAKE) | dict(table_stride=4, table_width=4, free_count=3, batch=2, page_size=16)
+    assert L.svdq_kv_plan(ctypes.byref(S._KvPlanDesc(*[{**plan, "rows": many}[n] for n in names])), None) == 2
+
+
 def test_python_refusals_without_a_gpu(S):
     """CPU tensors and wrong formats never reach the library."""
     with pytest.raises(TypeError):

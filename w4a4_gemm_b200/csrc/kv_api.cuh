@@ -134,6 +134,9 @@ int kv_geometry(const svdq_kv_cache* c, KvGeom* g, bool need_pool) {
   return SVDQ_OK;
 }
 
+// Rows that plan, append and read take: the kernels count rows, and CTAs of up to 1024 rows, in 32 bits.
+constexpr int kMaxRows = 1 << 30;
+
 // The grid of append or read, `values` to a piece, and the rows of a thread: several where there are enough pieces for
 // every thread that the SMs hold, so that more loads are in flight; one where latency counts.
 int append_grid(int M, const KvGeom& g, int values, int sms, dim3* grid) {
@@ -190,7 +193,7 @@ SVDQ_API int svdq_kv_page_bytes(const svdq_kv_cache* cache, size_t* bytes) {
 SVDQ_API int svdq_kv_plan(const svdq_kv_plan_desc* d, void* stream) {
   if (d == nullptr || d->batch < 0 || d->rows < 0 || d->table_width < 0 || d->free_count < 0 || d->table_stride < d->table_width)
     return SVDQ_ERR_INVALID_ARG;
-  if (d->batch > kPlanMaxRequests || d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)) != 0)
+  if (d->batch > kPlanMaxRequests || d->rows > kMaxRows || d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)) != 0)
     return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (d->cu_q == nullptr || d->used == nullptr || (d->batch > 0 && (d->q_lens == nullptr || d->kv_lens == nullptr || d->total_lens == nullptr)) ||
       (d->batch > 0 && d->table_width > 0 && d->block_table == nullptr) || (d->free_count > 0 && d->free_pages == nullptr) ||
@@ -285,6 +288,7 @@ SVDQ_API int svdq_kv_append(const svdq_kv_cache* cache, const void* k, const voi
   if (rc) return rc;
   if (M < 0) return SVDQ_ERR_INVALID_ARG;
   if (M == 0) return SVDQ_OK;
+  if (M > kMaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (slots == nullptr || !rows_ok(k, k_stride) || !rows_ok(v, v_stride)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
@@ -305,6 +309,7 @@ SVDQ_API int svdq_kv_read(const svdq_kv_cache* cache, const int64_t* slots, int 
   if (rc) return rc;
   if (M < 0) return SVDQ_ERR_INVALID_ARG;
   if (M == 0) return SVDQ_OK;
+  if (M > kMaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (slots == nullptr || k == nullptr || v == nullptr || !aligned16(k) || !aligned16(v)) return SVDQ_ERR_INVALID_ARG;
   int dev;
   if ((rc = kv_device(&dev))) return rc;
