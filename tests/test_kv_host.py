@@ -110,6 +110,12 @@ def test_refused_row_counts(S):
     assert L.svdq_kv_plan(ctypes.byref(S._KvPlanDesc(*[{**plan, "rows": many}[n] for n in names])), None) == 2
 
 
+def test_a_cache_keeps_its_pool(S):
+    """The calls hold the pool's address: a pool put in its place would be freed under it."""
+    with pytest.raises(AttributeError):
+        S.KVCache.__new__(S.KVCache).pool = torch.zeros(1, dtype=torch.uint8)
+
+
 def test_python_refusals_without_a_gpu(S):
     """CPU tensors and wrong formats never reach the library."""
     with pytest.raises(TypeError):

@@ -438,9 +438,14 @@ class KVCache:
 
     `pool` is uint8 [num_pages, kv_heads, block bytes], contiguous; without it
     one of `num_pages` pages is allocated on `device` (its contents are whatever
-    the memory held: tokens that were never appended are never read)."""
+    the memory held: tokens that were never appended are never read).  The calls
+    use the pool that the cache was made with: another one takes another KVCache."""
 
-    __slots__ = ("fmt", "kv_heads", "head_dim", "page_size", "pool", "num_pages", "page_bytes", "_c")
+    __slots__ = ("fmt", "kv_heads", "head_dim", "page_size", "_pool", "num_pages", "page_bytes", "_c")
+
+    @property
+    def pool(self) -> torch.Tensor:
+        return self._pool
 
     def __init__(self, fmt, kv_heads: int, head_dim: int, page_size: int, pool: Optional[torch.Tensor] = None,
                  num_pages: Optional[int] = None, device=None):
@@ -458,7 +463,7 @@ class KVCache:
         if type(r) is int:
             _check(r, "KVCache")
         self._c, self.page_bytes = r
-        self.pool, self.num_pages = pool, pool.shape[0]
+        self._pool, self.num_pages = pool, pool.shape[0]
 
 
 def svdq_kv_plan(q_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
