@@ -690,7 +690,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         bool more = w.count > 0, ok = true;
         const uint64_t qd = make_kmajor_desc(smem_u32(smem + L::kQ), 128), kd = make_kmajor_desc(smem_u32(smem + L::kK), 128);
         const uint64_t vd = make_sdesc(smem_u32(smem + L::kV), L::kPanel, 1024, kSwizzle128B);
-        auto& wait1 = wait;
         auto commit = [&](uint64_t* bar) {
           if (elect_one()) tc_commit(bar);
           __syncwarp();
@@ -720,9 +719,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
         };
         while (more && ok) {
           const int halves = w.rt * RT + 128 < w.req.n * p.rep.d ? 2 : 1;
-          ok = wait1(&k_full[tile % L::kKStages], (tile / L::kKStages) & 1);
+          ok = wait(&k_full[tile % L::kKStages], (tile / L::kKStages) & 1);
           for (int i = 0; i < halves && ok; ++i) {
-            ok = wait1(&q_full[i], qf[i]++ & 1);
+            ok = wait(&q_full[i], qf[i]++ & 1);
             if (!ok) break;
             tc_fence_after();
             scores(i, tile % L::kKStages);
@@ -733,15 +732,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) kv_attn_rows_kernel(const Att
             const bool next = j + 1 < w.here;
             const uint32_t ks = (tile + 1) % L::kKStages, vs = tile % L::kVStages;
             // what the code warps bring is there long before the weights
-            ok = wait1(&v_full[vs], (tile / L::kVStages) & 1) &&
-                 (!next || L::kKStages == 1 || wait1(&k_full[ks], ((tile + 1) / L::kKStages) & 1));
+            ok = wait(&v_full[vs], (tile / L::kVStages) & 1) &&
+                 (!next || L::kKStages == 1 || wait(&k_full[ks], ((tile + 1) / L::kKStages) & 1));
             for (int i = 0; i < halves && ok; ++i) {
-              ok = wait1(&p_full[i], pf[i]++ & 1);
+              ok = wait(&p_full[i], pf[i]++ & 1);
               if (!ok) break;
               tc_fence_after();
               values(i, vs, j == 0);
               if (L::kKStages == 1 && next && i == 0) {   // a single stage is filled behind the scores before it
-                ok = wait1(&k_full[ks], ((tile + 1) / L::kKStages) & 1);
+                ok = wait(&k_full[ks], ((tile + 1) / L::kKStages) & 1);
                 if (!ok) break;
                 tc_fence_after();
               }

@@ -7,8 +7,8 @@
 //   pairs: (2i, 2i + 1) interleaved, else (i, i + rot / 2), i < rot / 2
 //
 // fp32 from the load to the one rounding to bf16 at the store.
-// A head belongs to L = 4, 8, 16 or 32 neighbouring lanes (8 elements = 16 bytes
-// each), so a warp's loads and stores are whole lines, the mean is log2(L)
+// A head belongs to L = 2 to 32 neighbouring lanes (8 elements = 16 bytes each; L is the
+// power of two that holds them, the lanes past D / 8 idle), so a warp's loads and stores are whole lines, the mean is log2(L)
 // shuffles, and the half-split partner of an element sits in another lane at the
 // same place.  A lane group keeps its cosines, sines and weights in registers
 // over the heads of a row that it walks.
