@@ -39,6 +39,9 @@ bool dec_wide(const svdq_kv_attention_desc* d, int nb, int sms) {
 
 // The tcgen05 kernel takes the call where a key head has more than this many query rows per request on average: its
 // tiles have 256 rows.  16 requests over 8192 keys, 8 key heads: at 24 rows 64 us against 101, at 48 rows 96 against 98.
+// The rule looks at the call, whose lengths are not known here, not at each request: a call that mixes a long prompt with
+// single tokens is slower than one call for each (1500 tokens beside 64 single ones over up to 8192 keys: 452 us, apart
+// 56 and 81).
 constexpr int kRowsFrom = 48;
 bool many_rows(const svdq_kv_attention_desc* d) {
   return d->batch > 0 && static_cast<long long>(d->rows) * (d->q_heads / d->cache.kv_heads) > static_cast<long long>(kRowsFrom) * d->batch;

@@ -8,12 +8,13 @@
 // no key gives o = 0 and lse = -inf.
 //
 // The kernel of this file is for few query rows per key head (decode), which read the
-// cache once: 64 requests of 2048 to 8192 keys, 8 key heads of 128, NVFP4: 83 us, 4.7 TB/s;
-// 3 requests of 131000 keys, INT4: 102 us, 4.2 TB/s; one of 1000 keys: 11 us.  The
-// issue of instructions bounds it (about 280 per 16 keys and key head, of which 64
-// convert codes and 64 multiply them by scales; copies alone take 70 us where the whole
-// takes 83), then the ends of the items.  A warp takes 64 keys at a time, all D, from a ring of bulk
-// copies of its own, turns the codes into operand fragments in registers, and
+// cache once: 64 requests of 2048 to 8192 keys, 8 key heads of 128, NVFP4: 84 us, 4.7 TB/s (FP4 g32
+// 78, INT4 85); 3 requests of 131000 keys, INT4: 102 us, 4.2 TB/s; one of 1000 keys: 11 us.
+// Latency at low occupancy bounds it: 157 registers and 74 KB per CTA leave three warps to a scheduler,
+// each in one serial chain per 64 keys (wait, convert, scores, maximum, exp2, transpose, values).  Of the
+// first case's cycles the schedulers issue in 53 % (46 million instructions, about 270 per 16 keys and key
+// head), DRAM is busy in 54 %, the ALUs in 45 %; copies alone take 70 us.  Then the ends of the
+// items.  A warp takes 64 keys at a time, all D, from a ring of bulk copies of its own, turns the codes into operand fragments in registers, and
 // keeps a running maximum and sum per row; the warps of a CTA take turns along the
 // keys and join at the end of an item.  The products run transposed,
 //   S^T = K q^T,   O^T += V^T P^T,

@@ -13,8 +13,8 @@
 //
 // 4608 tokens of 24 heads attending to each other, NVFP4: 240 us, 1090 TFLOP/s; 3
 // prompts of up to 1500 tokens over up to 6000 keys, FP4 g32: 195 us, 690 TFLOP/s;
-// INT4, with its second product for the keys: 350 us and 232 us (561 and 317 with its
-// tiles worked out in fp32 instead of fp16 pairs).  A tile of 128 keys takes 3700 cycles,
+// INT4, with its second product for the keys: 337 us, and 3 such prompts of other lengths 238 us, 480
+// TFLOP/s (561 and 317 with its tiles worked out in fp32 instead of fp16 pairs).  A tile of 128 keys takes 3700 cycles,
 // 2048 of them on the tensor core; the chain scores - softmax -
 // values - scores of a half (2000 + 1100 + hand-offs) bounds it, and 13 to 20 thousand
 // cycles at each end of an item.
