@@ -485,6 +485,40 @@ def test_serving_steps(S, fmt):
     wqkv.close(), wout.close()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_serving_steps_with_a_window(S, fmt):
+    """A prompt and decode steps under a sliding window in a pool that holds a fraction of the tokens: pages that the
+    window has left go back to the free list, their entries become -1, and other tokens are written into them."""
+    hq, hk, D, page, window, batch = 4, 2, 64, 16, 20, 2
+    g = torch.Generator().manual_seed(17)
+    cache = S.KVCache(fmt, hk, D, page, num_pages=14)
+    table = torch.full((batch, 12), -1, dtype=torch.int32, device="cuda")
+    free, lens = list(range(14)), torch.zeros(batch, dtype=torch.int32, device="cuda")
+    held = [[np.zeros((0, hk, D))] * 2 for _ in range(batch)]
+    reused = set()
+    for step, new in enumerate([[60, 70]] + [[1, 2]] * 45):
+        q, k, v = (torch.randn(sum(new), h, D, generator=g).to(torch.bfloat16) for h in (hq, hk, hk))
+        cu, lens, pos, slots, used = S.svdq_kv_plan(torch.tensor(new, dtype=torch.int32, device="cuda"), lens, table,
+                                                    dev(free, torch.int32), sum(new), page)
+        reused |= {p for p in free[:int(used)] if step}
+        free = free[int(used):]
+        S.svdq_kv_append(cache, k.cuda(), v.cuda(), slots)
+        out = S.svdq_kv_attention(cache, q.cuda(), cu, lens, table, window=window)
+        at = 0
+        for b, n in enumerate(new):
+            for side, t in enumerate((k, v)):
+                held[b][side] = np.concatenate((held[b][side], R.quantize(fmt, t[at:at + n])[2]))
+            o, _, to, _ = R.attention(q[at:at + n].double().numpy(), *held[b], D ** -0.5, True, window, fmt == "int4")
+            within(out[at:at + n], o, to)
+            at += n
+        for b, kv in enumerate(lens.tolist()):
+            for col in range(max(0, kv + 1 - window) // page):      # the next query's first key
+                if int(table[b, col]) >= 0:
+                    free.append(int(table[b, col]))
+                    table[b, col] = -1
+    assert S.svdq_get_error() == 0 and lens.tolist() == [105, 160] and len(reused) > 5
+
+
 # ------------------------------------------------------ longer, split, together ---
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D,hq,hk,lens", [
